@@ -13,13 +13,16 @@ DF11_OK = 0
 DF11_MAX_TABLES = 64
 DF11_FAST_BITS_MAX = 12
 DF11_FAST_BITS_DEFAULT = 11
+DF11_BF16, DF11_FP16, DF11_FP32 = 0, 1, 2
+DF11_MAX_DIM = 256
+DF11_NO_TOKEN = 0x7fffffff
 DF11_Y_F32 = 0
 DF11_Y_BF16 = 1
 DF11_STORES_AUTO, DF11_STORES_CACHED, DF11_STORES_STREAMING = 0, 1, 2
 DF11_GEMM_AUTO, DF11_GEMM_SEGMENT, DF11_GEMM_WIDE, DF11_GEMM_TILED, DF11_GEMM_VECTOR, DF11_GEMM_PIPE, DF11_GEMM_RING = \
     0, 1, 2, 3, 4, 5, 6
 
-u32, u64 = ctypes.c_uint32, ctypes.c_uint64
+u32, u64, i64 = ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int64
 
 
 class Codebook(ctypes.Structure):
@@ -93,6 +96,9 @@ EXPORTS = (
     "df11_validate", "df11_decode", "df11_decode_batch", "df11_decode_batch_tuned", "df11_decode_rows",
     "df11_decode_gemm", "df11_decode_gemm_out", "df11_decode_gemm_ex", "df11_decode_gemm_noalloc", "df11_decode_gemm_workspace_bytes", "df11_decode_gemm_noalloc", "df11_hist_device", "df11_encode_device", "df11_device_encoded_free", "df11_device_encoded_view",
     "df11_device_encoded_to_host",
+    "df11_prefix_attention_workspace_bytes", "df11_prefix_attention", "df11_cache_attention_workspace_bytes",
+    "df11_cache_attention", "df11_cache_insert", "df11_cache_compact", "df11_verify_drafts_workspace_bytes",
+    "df11_verify_drafts",
     "df11_status_string", "df11_last_error", "df11_version",
 )
 
@@ -149,6 +155,18 @@ def lib():
     L.df11_device_encoded_free.restype = None
     L.df11_device_encoded_view.argtypes = [vp, ctypes.POINTER(View)]
     L.df11_device_encoded_to_host.argtypes = [vp, ctypes.POINTER(vp)]
+    # argument structs of the generation operators arrive packed (serve.py)
+    L.df11_prefix_attention_workspace_bytes.argtypes = [vp]
+    L.df11_prefix_attention.argtypes = [vp, vp, u64, vp]
+    L.df11_cache_attention_workspace_bytes.argtypes = [vp, vp]
+    L.df11_cache_attention.argtypes = [vp, vp, vp, u64, vp]
+    L.df11_cache_insert.argtypes = [vp, vp, vp, i64, i64, vp, i64, vp, vp, vp]
+    L.df11_cache_compact.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp]
+    L.df11_verify_drafts_workspace_bytes.argtypes = [vp]
+    L.df11_verify_drafts.argtypes = [vp, vp, u64, vp]
+    for name in ("df11_prefix_attention_workspace_bytes", "df11_cache_attention_workspace_bytes",
+                 "df11_verify_drafts_workspace_bytes"):
+        getattr(L, name).restype = u64
     L.df11_status_string.argtypes = [ctypes.c_int]
     L.df11_status_string.restype = ctypes.c_char_p
     L.df11_last_error.restype = ctypes.c_char_p
@@ -157,7 +175,9 @@ def lib():
                  "df11_gemm_layout", "df11_validate", "df11_decode", "df11_decode_batch", "df11_decode_batch_tuned",
                  "df11_decode_rows", "df11_decode_gemm", "df11_decode_gemm_out", "df11_decode_gemm_ex", "df11_decode_gemm_noalloc",
                  "df11_hist_device", "df11_encode_device",
-                 "df11_device_encoded_view", "df11_device_encoded_to_host"):
+                 "df11_device_encoded_view", "df11_device_encoded_to_host",
+                 "df11_prefix_attention", "df11_cache_attention", "df11_cache_insert", "df11_cache_compact",
+                 "df11_verify_drafts"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L

@@ -37,7 +37,7 @@ INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-HIP_SOURCES = ["decode.hip", "decode_gemm.hip", "encode.hip"]
+HIP_SOURCES = ["decode.hip", "decode_gemm.hip", "encode.hip", "attention.hip", "cache.hip", "verify.hip"]
 CPP_SOURCES = ["host_codebook.cpp", "host_encode.cpp", "host_validate.cpp"]
 
 # Packed FP32 instructions are kept out of every HIP object.

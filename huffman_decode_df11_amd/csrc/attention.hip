@@ -1,0 +1,626 @@
+// Attention of a generation step: over a prefix that a batch of sequences
+// shares (df11_prefix_attention) and over a bounded cache whose slots add up
+// the attention they get (df11_cache_attention).
+//
+// For a row q (one query token of one head) and its keys K_j, values V_j:
+//   s_j = scale * q . K_j,   o = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m),
+// taken in one pass with the running maximum m and the running sum l: a new
+// maximum m' scales the sums so far by exp(m - m').  A range of keys thus
+// gives (m, l, o) on its own, and ranges are joined the same way, so the
+// keys are split over workgroups and over a workgroup's waves.  Logarithms
+// are to base 2: exp(x) = 2^(x log2 e) is one instruction.
+//
+// attend_wave: one wave, 16 rows, 32 keys at a time, no LDS.
+//   S^T = K Q^T  v_mfma_f32_16x16x32: the A operand of lane l is key l % 16,
+//                dims 8 * (4 i + l / 16) .. + 7 of step i, as they lie in
+//                memory; the B operand the same dims of row l % 16.
+//   P^T          lane l holds row l % 16 and the keys 4 (l / 16) + 0..3 of
+//                each of two 16-key tiles: 8 keys, just the B operand of one
+//                32-key step of
+//   O^T = V^T P^T  whose A operand wants, for one dim, those 8 keys side by
+//                side.  Each lane loads its 8 keys' dims (l % 16) W .. + W - 1
+//                (W = dims / 16; a wave reads whole rows of V) and turns the
+//                8 x W block in registers (v_perm_b32); product j of the W
+//                takes the dims j, W + j, 2 W + j, ...
+#include <algorithm>
+
+#include "df11_internal.h"
+#include "serve_device.h"
+
+namespace {
+
+using namespace df11serve;
+
+constexpr int kWaves = 4;      // waves of a workgroup, each on every fourth run of 32 keys
+constexpr int kRows = 16;      // rows of a tile
+constexpr int kStep = 32;      // keys of a step
+
+struct Args {
+    const uint16_t *q, *prefix_k, *prefix_v, *k, *v;
+    const int32_t *lengths, *table, *pos, *positions;
+    uint16_t *out;
+    float *lse, *weights;
+    float *part_o;             // [slot][row][dim]
+    float2 *part_ml;           // [slot][row]
+    float *logits;             // cache: [batch * kv_heads][rows of a head][logit_stride]
+    int32_t batch, tokens, heads, kv_heads, group, dim, prefix, suffix, page, n_pages, fp16;
+    int64_t q_batch, q_token, q_head, prefix_token, prefix_head, k_batch, k_token, k_head, table_batch;
+    int64_t logit_stride;
+    float scale2;              // scale * log2(e)
+    int32_t prefix_splits, prefix_span, prefix_tiles, suffix_splits, suffix_span, suffix_tiles;
+    int64_t rows;              // batch * tokens * heads
+};
+
+// The 32 keys from `base` on: rows in memory, and which of them which query
+// tokens see.  Lane l speaks for key base + l % 32: rel is the key's place
+// relative to the first query token (token t sees it when rel <= t).
+struct Keys {
+    uint32_t any, all;   // keys that some / every query token sees
+    int32_t rel;
+    int64_t row;         // element offset of lane l % 32's key
+};
+
+struct PrefixSource {
+    const uint16_t *k, *v;
+    int64_t token;
+    int32_t n;
+    __device__ __forceinline__ Keys keys(int base, int lane) const
+    {
+        const int left = n - base;
+        const uint32_t m = left >= 32 ? 0xffffffffu : (1u << left) - 1;
+        return Keys{m, m, 0, 0};
+    }
+    __device__ __forceinline__ int64_t at(const Keys &, int base, int i) const
+    {
+        return (int64_t)min(base + i, n - 1) * token;
+    }
+    __device__ __forceinline__ void logits(int, int, int, f32x4) const {}
+};
+
+struct SuffixSource {
+    const uint16_t *k, *v;
+    const int32_t *table;
+    int64_t batch, token;
+    int32_t n, tokens, page, n_pages;
+    __device__ __forceinline__ Keys keys(int base, int lane) const
+    {
+        const int key = base + (lane & 31);
+        const int32_t rel = key - (n - tokens);
+        bool there = key < n;
+        int64_t row = (int64_t)min(key, n - 1) * token;
+        if (table) {
+            const int p = min(key, n - 1) / page;
+            int32_t id = table[p];
+            there = there && id >= 0 && id < n_pages;
+            id = there ? id : 0;
+            row = (int64_t)id * batch + (int64_t)(min(key, n - 1) - p * page) * token;
+        }
+        return Keys{(uint32_t)__ballot(there), (uint32_t)__ballot(there && rel <= 0), rel, row};
+    }
+    __device__ __forceinline__ int64_t at(const Keys &m, int base, int i) const
+    {
+        return table ? __shfl(m.row, i) : (int64_t)min(base + i, n - 1) * token;
+    }
+    __device__ __forceinline__ void logits(int, int, int, f32x4) const {}
+};
+
+struct CacheSource {
+    const uint16_t *k, *v;
+    const int32_t *positions;
+    float *out;          // this row tile's logits
+    int64_t token, stride;
+    int32_t n, tokens, pos, row_count;
+    __device__ __forceinline__ Keys keys(int base, int lane) const
+    {
+        const int key = base + (lane & 31);
+        const bool in = key < n;
+        const int32_t p = in ? positions[key] : -1;
+        const bool some = p >= 0 && (int64_t)p <= (int64_t)pos + tokens - 1;
+        const int32_t rel = some ? p - pos : 0x7fffffff;
+        return Keys{(uint32_t)__ballot(some), (uint32_t)__ballot(some && rel <= 0), rel, 0};
+    }
+    __device__ __forceinline__ int64_t at(const Keys &, int base, int i) const
+    {
+        return (int64_t)min(base + i, n - 1) * token;
+    }
+    // the logits of row `row`, keys key .. key + 3
+    __device__ __forceinline__ void logits(int base, int row, int key, f32x4 s) const
+    {
+        if (row < row_count) *(f32x4 *)(out + row * stride + base + key) = s;
+    }
+};
+
+// One wave over the keys [key0, key1) of `src`, every `step`-th run of 32.
+// q: this lane's row as B operands; t: its query token.  o[j][r] is, for row
+// lane % 16, dim (4 (lane / 16) + r) * W + j of the sum; m and l its maximum
+// and its sum over this lane's keys.
+template <class E, int DP, class Src>
+__device__ __forceinline__ void attend_wave(const Src &src, const u32x4 (&q)[DP / 32], int t, int tokens, int dim,
+                                            int key0, int key1, int step, float scale2, f32x4 (&o)[DP / 16], float &m,
+                                            float &l)
+{
+    constexpr int W = DP / 16;
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    m = -INFINITY;
+    l = 0.0f;
+#pragma unroll
+    for (int j = 0; j < W; j++) o[j] = f32x4{0, 0, 0, 0};
+    for (int base = key0; base < key1; base += step) {
+        const Keys keys = src.keys(base, lane);
+        f32x4 s[2];
+        u32x4 kx[2][DP / 32];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int64_t row = src.at(keys, base, 16 * h + c);
+#pragma unroll
+            for (int i = 0; i < DP / 32; i++) {
+                const int d = 8 * (4 * i + g);
+                kx[h][i] = d < dim ? *(const u32x4 *)(src.k + row + d) : u32x4{0, 0, 0, 0};
+            }
+        }
+        uint32_t vx[8][W / 2];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int64_t row = src.at(keys, base, 16 * (j >> 2) + 4 * g + (j & 3));
+            const int d = c * W;
+            if constexpr (W == 4) {
+                const u32x2 x = d < dim ? *(const u32x2 *)(src.v + row + d) : u32x2{0, 0};
+                vx[j][0] = x[0], vx[j][1] = x[1];
+            } else {
+#pragma unroll
+                for (int w = 0; w < W / 8; w++) {
+                    const u32x4 x = d + 8 * w < dim ? *(const u32x4 *)(src.v + row + d + 8 * w) : u32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int y = 0; y < 4; y++) vx[j][4 * w + y] = x[y];
+                }
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            s[h] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < DP / 32; i++) s[h] = E::mfma16(kx[h][i], q[i], s[h]);
+        }
+        const bool plain = keys.any == keys.all;   // uniform
+        float mx = m;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const int i = 16 * h + 4 * g + r;
+                bool sees = (keys.any >> i) & 1;
+                if (!plain) {
+                    const int32_t rel = __shfl(keys.rel, i);   // of every lane's key, seen or not
+                    sees = sees && rel <= t;
+                }
+                s[h][r] = sees ? s[h][r] * scale2 : -INFINITY;
+                mx = fmaxf(mx, s[h][r]);
+            }
+            src.logits(base, c, 16 * h + 4 * g, s[h]);
+        }
+        mx = fmaxf(mx, __shfl_xor(mx, 16));
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        const float safe = mx == -INFINITY ? 0.0f : mx;
+        const float keep = exp2_fast(m - safe);
+        m = mx;
+        l *= keep;
+        float p[8];
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                p[4 * h + r] = exp2_fast(s[h][r] - safe);
+                l += p[4 * h + r];
+            }
+#pragma unroll
+        for (int j = 0; j < W; j++) o[j] *= keep;
+        // a key that no row of the tile sees takes part with weight 0: its
+        // value must be a number
+        if (keys.any != 0xffffffffu) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const bool sees = (keys.any >> (16 * (j >> 2) + 4 * g + (j & 3))) & 1;
+#pragma unroll
+                for (int w = 0; w < W / 2; w++) vx[j][w] = sees ? vx[j][w] : 0;
+            }
+        }
+        // The rows of different query tokens see different keys here.  A
+        // number times weight 0 is 0; only where a value that some rows must
+        // not see is not a number, the tokens take turns, each with its
+        // unseen keys cleared and the sums of its own rows kept.
+        int turns = 1;
+        if (!plain) {
+            bool odd = false;
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+#pragma unroll
+                for (int w = 0; w < W / 2; w++)
+                    odd = odd || (vx[j][w] & E::kExpMask) == E::kExpMask ||
+                          ((vx[j][w] >> 16) & E::kExpMask) == E::kExpMask;
+            if (__any(odd)) turns = tokens;
+        }
+        int32_t rel[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) rel[j] = plain ? 0 : __shfl(keys.rel, 16 * (j >> 2) + 4 * g + (j & 3));
+        for (int turn = 0; turn < turns; turn++) {
+            const bool mine = turns == 1 || t == turn;
+            u32x4 pb;
+#pragma unroll
+            for (int w = 0; w < 4; w++) pb[w] = E::pack(p[2 * w], p[2 * w + 1]);
+#pragma unroll
+            for (int j = 0; j < W; j++) {
+                u32x4 va;
+#pragma unroll
+                for (int w = 0; w < 4; w++) {
+                    uint32_t lo = vx[2 * w][j / 2], hi = vx[2 * w + 1][j / 2];
+                    if (turns > 1) {
+                        lo = rel[2 * w] <= turn ? lo : 0;
+                        hi = rel[2 * w + 1] <= turn ? hi : 0;
+                    }
+                    va[w] = __builtin_amdgcn_perm(hi, lo, j & 1 ? 0x07060302u : 0x05040100u);
+                }
+                const f32x4 sum = E::mfma16(va, pb, o[j]);
+#pragma unroll
+                for (int r = 0; r < 4; r++) o[j][r] = mine ? sum[r] : o[j][r];
+            }
+        }
+    }
+}
+
+// One workgroup: a tile of 16 rows over one range of keys.  Workgroups below
+// the prefix count take a tile of all sequences' rows of one key head over a
+// range of the prefix, the others a tile of one sequence's rows of one key
+// head over a range of its own positions (or of its cache).
+template <class E, int DP, bool CACHE>
+__global__ void __launch_bounds__(64 * kWaves) attend_kernel(const Args a)
+{
+    constexpr int W = DP / 16;
+    __shared__ float join_o[kWaves][kRows][DP + 4];
+    __shared__ float2 join_ml[kWaves][kRows];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+    const int prefix_items = a.kv_heads * a.prefix_tiles * a.prefix_splits;
+    int item = blockIdx.x;
+    const bool in_prefix = !CACHE && item < prefix_items;
+    int split, tile, head, b = 0;
+    if (in_prefix) {
+        split = item % a.prefix_splits, item /= a.prefix_splits;
+        tile = item % a.prefix_tiles, head = item / a.prefix_tiles;
+    } else {
+        item -= CACHE ? 0 : prefix_items;
+        split = item % a.suffix_splits, item /= a.suffix_splits;
+        tile = item % a.suffix_tiles, item /= a.suffix_tiles;
+        head = item % a.kv_heads, b = item / a.kv_heads;
+    }
+    const int row_count = (in_prefix ? a.batch : 1) * a.tokens * a.group;
+    const int span = in_prefix ? a.prefix_span : a.suffix_span;
+    const int n = in_prefix ? a.prefix : max(0, min(a.lengths[b], a.suffix));
+    const int key0 = split * span, key1 = min(n, key0 + span);
+    if (key0 >= key1) return;   // the join knows from n that there is no such range
+
+    // row r of a tile: sequence, query token, head of the group
+    const int row = tile * kRows + c;
+    const int t = row / a.group % a.tokens;
+    const int rb = in_prefix ? row / (a.group * a.tokens) : b;
+    const int h = head * a.group + row % a.group;
+    u32x4 q[DP / 32];
+#pragma unroll
+    for (int i = 0; i < DP / 32; i++) {
+        const int d = 8 * (4 * i + g);
+        q[i] = row < row_count && d < a.dim
+                   ? *(const u32x4 *)(a.q + rb * a.q_batch + t * a.q_token + h * a.q_head + d)
+                   : u32x4{0, 0, 0, 0};
+    }
+    f32x4 o[W];
+    float m, l;
+    const int first = key0 + kStep * wave;
+    if constexpr (CACHE) {
+        const int64_t bh = (int64_t)b * a.kv_heads + head;
+        const int64_t at = b * a.k_batch + head * a.k_head;
+        const CacheSource src{a.k + at, a.v + at, a.positions + bh * a.suffix,
+                              a.logits + (bh * row_count + tile * kRows) * a.logit_stride, a.k_token, a.logit_stride, n,
+                              a.tokens, a.pos[b], row_count - tile * kRows};
+        attend_wave<E, DP>(src, q, t, a.tokens, a.dim, first, key1, kStep * kWaves, a.scale2, o, m, l);
+    } else if (in_prefix) {
+        const PrefixSource src{a.prefix_k + head * a.prefix_head, a.prefix_v + head * a.prefix_head, a.prefix_token, n};
+        attend_wave<E, DP>(src, q, t, a.tokens, a.dim, first, key1, kStep * kWaves, a.scale2, o, m, l);
+    } else {
+        const int64_t at = (a.table ? 0 : b * a.k_batch) + head * a.k_head;
+        const SuffixSource src{a.k + at, a.v + at, a.table ? a.table + b * a.table_batch : nullptr, a.k_batch,
+                               a.k_token, n, a.tokens, a.page, a.n_pages};
+        attend_wave<E, DP>(src, q, t, a.tokens, a.dim, first, key1, kStep * kWaves, a.scale2, o, m, l);
+    }
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (g == 0) join_ml[wave][c] = make_float2(m, l);
+#pragma unroll
+    for (int r = 0; r < 4; r++)
+#pragma unroll
+        for (int j = 0; j < W; j++) join_o[wave][c][(4 * g + r) * W + j] = o[j][r];
+    __syncthreads();
+    const int slot = in_prefix ? split : a.prefix_splits + split;
+    for (int i = threadIdx.x; i < kRows * DP; i += 64 * kWaves) {
+        const int r = i / DP, d = i % DP, at = tile * kRows + r;
+        if (at >= row_count || d >= a.dim) continue;
+        float mm = -INFINITY, ll = 0.0f, oo = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; w++) mm = fmaxf(mm, join_ml[w][r].x);
+        const float safe = mm == -INFINITY ? 0.0f : mm;
+#pragma unroll
+        for (int w = 0; w < kWaves; w++) {
+            const float f = exp2_fast(join_ml[w][r].x - safe);
+            ll += f * join_ml[w][r].y;
+            oo += f * join_o[w][r][d];
+        }
+        const int tt = at / a.group % a.tokens, bb = in_prefix ? at / (a.group * a.tokens) : b;
+        const int64_t out_row = ((int64_t)bb * a.tokens + tt) * a.heads + head * a.group + at % a.group;
+        a.part_o[(slot * a.rows + out_row) * a.dim + d] = oo;
+        if (d == 0) a.part_ml[slot * a.rows + out_row] = make_float2(mm, ll);
+    }
+}
+
+// Ranges of a row's own positions that hold any.
+__device__ __forceinline__ int own_splits(const Args &a, int b)
+{
+    const int n = max(0, min(a.lengths[b], a.suffix));
+    return (n + a.suffix_span - 1) / a.suffix_span;
+}
+
+// The joined maximum and sum of an output row.
+__device__ __forceinline__ float2 join_row(const Args &a, int64_t row, int own)
+{
+    float m = -INFINITY, l = 0.0f;
+    for (int s = 0; s < a.prefix_splits + own; s++) m = fmaxf(m, a.part_ml[s * a.rows + row].x);
+    const float safe = m == -INFINITY ? 0.0f : m;
+    for (int s = 0; s < a.prefix_splits + own; s++) {
+        const float2 x = a.part_ml[s * a.rows + row];
+        l += exp2_fast(x.x - safe) * x.y;
+    }
+    return make_float2(m, l);
+}
+
+// One wave joins the ranges of one output row.
+template <class E>
+__global__ void __launch_bounds__(256) join_kernel(const Args a)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= a.rows) return;
+    const int b = (int)(row / ((int64_t)a.tokens * a.heads));
+    const int own = own_splits(a, b);
+    const float2 ml = join_row(a, row, own);
+    const float safe = ml.x == -INFINITY ? 0.0f : ml.x;
+    const float inv = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
+    for (int d = 2 * lane; d < a.dim; d += 128) {
+        float x = 0.0f, y = 0.0f;
+        for (int s = 0; s < a.prefix_splits + own; s++) {
+            const float f = exp2_fast(a.part_ml[s * a.rows + row].x - safe);
+            const float2 o = *(const float2 *)(a.part_o + (s * a.rows + row) * a.dim + d);
+            x += f * o.x, y += f * o.y;
+        }
+        *(uint32_t *)(a.out + row * a.dim + d) = E::pack(x * inv, y * inv);
+    }
+    if (a.lse && lane == 0) a.lse[row] = ml.y == 0.0f ? -INFINITY : kLn2 * (ml.x + __log2f(ml.y));
+}
+
+// A slot's weight: the probabilities that the rows of its head gave it.
+__global__ void __launch_bounds__(256) weigh_kernel(const Args a)
+{
+    __shared__ float top[256];
+    const int bh = blockIdx.y, b = bh / a.kv_heads, head = bh % a.kv_heads;
+    const int n = max(0, min(a.lengths[b], a.suffix));
+    const int key = blockIdx.x * 256 + threadIdx.x;
+    if ((int)(blockIdx.x * 256) >= n) return;
+    const int row_count = a.tokens * a.group, own = own_splits(a, b);
+    float w = 0.0f;
+    for (int r0 = 0; r0 < row_count; r0 += 256) {
+        __syncthreads();
+        const int r = r0 + threadIdx.x;
+        if (r < row_count) {
+            const int64_t row = ((int64_t)b * a.tokens + r / a.group) * a.heads + head * a.group + r % a.group;
+            const float2 ml = join_row(a, row, own);
+            top[threadIdx.x] = ml.y == 0.0f ? INFINITY : ml.x + __log2f(ml.y);   // an empty row gives nothing
+        }
+        __syncthreads();
+        if (key < n)
+            for (int i = 0; i < min(256, row_count - r0); i++)
+                w += exp2_fast(a.logits[((int64_t)bh * row_count + r0 + i) * a.logit_stride + key] - top[i]);
+    }
+    if (key < n) a.weights[(int64_t)bh * a.suffix + key] += w;
+}
+
+int ceil_div(int64_t x, int64_t y) { return (int)((x + y - 1) / y); }
+
+// Ranges of at least 256 keys, enough of them for `want` workgroups in all.
+void plan_splits(int64_t keys, int64_t items, int64_t want, int32_t *splits, int32_t *span)
+{
+    const int64_t most = std::max<int64_t>(1, keys / 256);
+    const int64_t n = std::max<int64_t>(1, std::min(most, want / std::max<int64_t>(1, items)));
+    *span = ceil_div(ceil_div(std::max<int64_t>(keys, 1), n), kStep * kWaves) * kStep * kWaves;
+    *splits = keys ? ceil_div(keys, *span) : 0;
+}
+
+void plan(Args &a)
+{
+    const int64_t want = 8 * df11::cu_count();
+    a.rows = (int64_t)a.batch * a.tokens * a.heads;
+    a.prefix_tiles = ceil_div((int64_t)a.batch * a.tokens * a.group, kRows);
+    a.suffix_tiles = ceil_div((int64_t)a.tokens * a.group, kRows);
+    plan_splits(a.prefix, (int64_t)a.prefix_tiles * a.kv_heads, want, &a.prefix_splits, &a.prefix_span);
+    plan_splits(a.suffix, (int64_t)a.suffix_tiles * a.kv_heads * a.batch, want, &a.suffix_splits, &a.suffix_span);
+}
+
+int64_t part_bytes(const Args &a)
+{
+    const int64_t slots = a.prefix_splits + a.suffix_splits;
+    return slots * a.rows * (8 + 4ll * a.dim);
+}
+
+bool small(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
+
+constexpr int64_t kMost = 1ll << 30;
+
+int check_heads(const char *who, int64_t dtype, int64_t batch, int64_t tokens, int64_t heads, int64_t kv_heads,
+                int64_t dim)
+{
+    if (dtype != DF11_BF16 && dtype != DF11_FP16) return df11::fail(DF11_E_ARG, "%s: dtype must be bf16 or fp16", who);
+    if (!small(dim, 8, DF11_MAX_DIM) || dim % 8)
+        return df11::fail(DF11_E_ARG, "%s: dim %lld is not a multiple of 8 up to %d", who, (long long)dim, DF11_MAX_DIM);
+    if (!small(kv_heads, 1, 65535) || !small(heads, 1, kMost) || heads % kv_heads)
+        return df11::fail(DF11_E_ARG, "%s: %lld heads are no multiple of %lld key heads", who, (long long)heads,
+                          (long long)kv_heads);
+    if (!small(batch, 0, kMost) || !small(tokens, 1, 65536) || (double)batch * tokens * heads > kMost)
+        return df11::fail(DF11_E_ARG, "%s: batch %lld of %lld tokens out of range", who, (long long)batch,
+                          (long long)tokens);
+    return DF11_OK;
+}
+
+int strides_ok(const char *who, std::initializer_list<int64_t> strides)
+{
+    for (int64_t s : strides)
+        if (s < 0 || s % 8) return df11::fail(DF11_E_ARG, "%s: stride %lld is not a multiple of 8", who, (long long)s);
+    return DF11_OK;
+}
+
+template <class E, bool CACHE>
+int launch(const Args &a, hipStream_t st)
+{
+    const int64_t items = (CACHE ? 0 : (int64_t)a.kv_heads * a.prefix_tiles * a.prefix_splits) +
+                          (int64_t)a.batch * a.kv_heads * a.suffix_tiles * a.suffix_splits;
+    if (items > 0x7fffffffll) return df11::fail(DF11_E_ARG, "attention: too many rows and keys for one launch");
+    const dim3 grid((uint32_t)items), block(64 * kWaves);
+    if (items) {
+        if (a.dim <= 64) hipLaunchKernelGGL((attend_kernel<E, 64, CACHE>), grid, block, 0, st, a);
+        else if (a.dim <= 128) hipLaunchKernelGGL((attend_kernel<E, 128, CACHE>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((attend_kernel<E, 256, CACHE>), grid, block, 0, st, a);
+    }
+    hipLaunchKernelGGL((join_kernel<E>), dim3((uint32_t)((a.rows + 3) / 4)), dim3(256), 0, st, a);
+    if (CACHE && a.suffix)
+        hipLaunchKernelGGL(weigh_kernel, dim3(ceil_div(a.suffix, 256), a.batch * a.kv_heads), dim3(256), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return df11::fail(DF11_E_DEVICE, "attention launch: %s", hipGetErrorString(e));
+    return DF11_OK;
+}
+
+int check_workspace(const char *who, void *ws, uint64_t bytes, uint64_t need)
+{
+    if (bytes < need || (need && !aligned16(ws)))
+        return df11::fail(DF11_E_ARG, "%s: the workspace must be 16-byte aligned and hold %llu bytes", who,
+                          (unsigned long long)need);
+    return DF11_OK;
+}
+
+void place(Args &a, void *ws)
+{
+    const int64_t slots = a.prefix_splits + a.suffix_splits;
+    a.part_o = (float *)ws;
+    a.part_ml = (float2 *)(a.part_o + slots * a.rows * a.dim);
+    a.logits = (float *)((char *)ws + (part_bytes(a) + 15) / 16 * 16);
+}
+
+int make_prefix(const df11_prefix_attention_args *p, Args &a)
+{
+    const char *who = "df11_prefix_attention";
+    if (!p) return df11::fail(DF11_E_ARG, "%s: null arguments", who);
+    int rc = check_heads(who, p->dtype, p->batch, p->tokens, p->heads, p->kv_heads, p->dim);
+    if (rc) return rc;
+    if (!small(p->prefix, 0, kMost) || !small(p->suffix, 0, kMost) ||
+        (p->block_table && (!small(p->page, 1, kMost) || !small(p->n_pages, 0, kMost) || p->suffix % p->page)))
+        return df11::fail(DF11_E_ARG, "%s: prefix, suffix or page sizes out of range", who);
+    rc = strides_ok(who, {p->q_batch, p->q_token, p->q_head, p->prefix_token, p->prefix_head, p->k_batch, p->k_token,
+                          p->k_head});
+    if (rc) return rc;
+    if (p->table_batch < 0) return df11::fail(DF11_E_ARG, "%s: negative table stride", who);
+    a.q = (const uint16_t *)p->q;
+    a.prefix_k = (const uint16_t *)p->prefix_k, a.prefix_v = (const uint16_t *)p->prefix_v;
+    a.k = (const uint16_t *)p->k, a.v = (const uint16_t *)p->v;
+    a.lengths = p->lengths, a.table = p->block_table;
+    a.out = (uint16_t *)p->out, a.lse = p->lse;
+    a.batch = p->batch, a.tokens = p->tokens, a.heads = p->heads, a.kv_heads = p->kv_heads;
+    a.group = p->heads / p->kv_heads, a.dim = p->dim, a.prefix = p->prefix;
+    a.suffix = p->block_table && !p->n_pages ? 0 : p->suffix;
+    a.page = p->block_table ? p->page : 1, a.n_pages = p->n_pages;
+    a.q_batch = p->q_batch, a.q_token = p->q_token, a.q_head = p->q_head;
+    a.prefix_token = p->prefix_token, a.prefix_head = p->prefix_head;
+    a.k_batch = p->k_batch, a.k_token = p->k_token, a.k_head = p->k_head, a.table_batch = p->table_batch;
+    a.scale2 = (float)(p->scale * 1.44269504088896340736);
+    plan(a);
+    return DF11_OK;
+}
+
+int make_cache(const df11_cache *c, const df11_cache_attention_args *p, Args &a)
+{
+    const char *who = "df11_cache_attention";
+    if (!c || !p) return df11::fail(DF11_E_ARG, "%s: null arguments", who);
+    int rc = check_heads(who, c->dtype, c->batch, p->tokens, p->heads, c->kv_heads, c->dim);
+    if (rc) return rc;
+    if (!small(c->slots, 0, kMost) || (double)c->batch * c->kv_heads > 65535)
+        return df11::fail(DF11_E_ARG, "%s: slots or batch * kv_heads out of range", who);
+    rc = strides_ok(who, {p->q_batch, p->q_token, p->q_head, c->stride_batch, c->stride_head, c->stride_slot});
+    if (rc) return rc;
+    a.q = (const uint16_t *)p->q;
+    a.k = (const uint16_t *)c->k, a.v = (const uint16_t *)c->v;
+    a.lengths = c->lengths, a.pos = p->pos, a.positions = c->positions, a.weights = c->weights;
+    a.out = (uint16_t *)p->out;
+    a.batch = c->batch, a.tokens = p->tokens, a.heads = p->heads, a.kv_heads = c->kv_heads;
+    a.group = p->heads / c->kv_heads, a.dim = c->dim, a.suffix = c->slots, a.page = 1;
+    a.q_batch = p->q_batch, a.q_token = p->q_token, a.q_head = p->q_head;
+    a.k_batch = c->stride_batch, a.k_token = c->stride_slot, a.k_head = c->stride_head;
+    a.scale2 = (float)(p->scale * 1.44269504088896340736);
+    plan(a);
+    a.logit_stride = (c->slots + 31) / 32 * 32;
+    return DF11_OK;
+}
+
+uint64_t cache_bytes(const Args &a)
+{
+    return (part_bytes(a) + 15) / 16 * 16 + 4ull * a.batch * a.kv_heads * a.tokens * a.group * a.logit_stride;
+}
+
+}  // namespace
+
+extern "C" uint64_t df11_prefix_attention_workspace_bytes(const df11_prefix_attention_args *p)
+{
+    Args a{};
+    return make_prefix(p, a) ? 0 : (uint64_t)part_bytes(a);
+}
+
+extern "C" int df11_prefix_attention(const df11_prefix_attention_args *p, void *workspace, uint64_t workspace_bytes,
+                                     void *stream)
+{
+    const char *who = "df11_prefix_attention";
+    Args a{};
+    int rc = make_prefix(p, a);
+    if (rc) return rc;
+    if (!a.rows) return DF11_OK;
+    if (!aligned16(a.q) || !aligned16(a.out) || !a.lengths || (a.prefix && (!aligned16(a.prefix_k) || !aligned16(a.prefix_v))) ||
+        (a.suffix && (!aligned16(a.k) || !aligned16(a.v))))
+        return df11::fail(DF11_E_ARG, "%s: null or misaligned pointer", who);
+    rc = check_workspace(who, workspace, workspace_bytes, part_bytes(a));
+    if (rc) return rc;
+    place(a, workspace);
+    return p->dtype == DF11_FP16 ? launch<Fp16, false>(a, (hipStream_t)stream)
+                                 : launch<Bf16, false>(a, (hipStream_t)stream);
+}
+
+extern "C" uint64_t df11_cache_attention_workspace_bytes(const df11_cache *c, const df11_cache_attention_args *p)
+{
+    Args a{};
+    return make_cache(c, p, a) ? 0 : cache_bytes(a);
+}
+
+extern "C" int df11_cache_attention(const df11_cache *c, const df11_cache_attention_args *p, void *workspace,
+                                    uint64_t workspace_bytes, void *stream)
+{
+    const char *who = "df11_cache_attention";
+    Args a{};
+    int rc = make_cache(c, p, a);
+    if (rc) return rc;
+    if (!a.rows) return DF11_OK;
+    if (!aligned16(a.q) || !aligned16(a.out) || !a.lengths || !a.pos ||
+        (a.suffix && (!aligned16(a.k) || !aligned16(a.v) || !a.weights || !a.positions)))
+        return df11::fail(DF11_E_ARG, "%s: null or misaligned pointer", who);
+    rc = check_workspace(who, workspace, workspace_bytes, cache_bytes(a));
+    if (rc) return rc;
+    place(a, workspace);
+    return c->dtype == DF11_FP16 ? launch<Fp16, true>(a, (hipStream_t)stream) : launch<Bf16, true>(a, (hipStream_t)stream);
+}

@@ -436,6 +436,157 @@ int df11_decode_gemm_ex(const df11_view *device_view, const uint16_t *x, uint32_
 int df11_decode_gemm_noalloc(const df11_view *device_view, const uint16_t *x, uint32_t B, void *y,
                              int y_dtype, uint16_t *w_debug, const df11_gemm_tuning *tuning, void *stream);
 
+/* ------------------------------------------------------- token generation */
+
+/* The operators of one generation step around the compressed weights ([P2]
+ * "工作原理": compressed weights serve token generation; [P1] 2.2 item 3):
+ * attention for sequences that share a prefix, attention over a bounded
+ * cache that evicts by accumulated attention weight, and the verification
+ * of drafted tokens.  All pointers are device memory of the current device;
+ * the work is asynchronous on `stream`; nothing is allocated.  Every field
+ * of the argument structs is 8 bytes wide, strides are in elements, and
+ * the last axis (dim, vocabulary) is contiguous.  A call that has nothing
+ * to compute (batch 0) launches nothing. */
+
+/* Element types of the operands below. */
+#define DF11_BF16 0
+#define DF11_FP16 1
+#define DF11_FP32 2   /* probabilities only */
+
+#define DF11_MAX_DIM 256
+#define DF11_NO_TOKEN 0x7fffffff   /* position of a cache slot that holds no token */
+
+/* Attention of `batch` sequences, `tokens` query tokens each, over a prefix
+ * that all of them share followed by each sequence's own positions:
+ *
+ *   o[b,t,h] = sum_j softmax_j(scale * q[b,t,h] . K_j) V_j,   h' = h / (heads / kv_heads)
+ *
+ * over the keys K_j of prefix_k[0..prefix)[h'] and of the sequence's own
+ * first lengths[b] - (tokens - 1) + t positions [h'] (the `tokens` query tokens are
+ * the last of those lengths[b] positions and see each other causally; a
+ * length outside [0, suffix] is taken as the nearer end).  A row without a
+ * visible key is zero, its lse -infinity.  The prefix is read once for all
+ * sequences, not once for each.  Own positions are [batch, suffix] rows
+ * (block_table NULL: k_batch, k_token, k_head strides) or lie in pages:
+ * position s of sequence b is row s % page of page
+ * block_table[b * table_batch + s / page] (k_batch is then the stride
+ * between pages, suffix = pages per sequence * page); a page id outside
+ * [0, n_pages) holds no visible position.  K and V share their strides.
+ * What masked or unused positions hold, NaN and infinities included, does not reach the output.
+ * Statistics and sums are float32; the probabilities are rounded to the
+ * operands' type for the product with V. */
+typedef struct df11_prefix_attention_args {
+    const void *q, *prefix_k, *prefix_v, *k, *v;
+    const int32_t *lengths;       /* [batch] */
+    const int32_t *block_table;   /* [batch, suffix / page], or NULL */
+    void *out;                    /* [batch, tokens, heads, dim], contiguous, the type of q */
+    float *lse;                   /* [batch, tokens, heads] natural log of the sum, or NULL */
+    int64_t dtype, batch, tokens, heads, kv_heads, dim, prefix, suffix, page, n_pages;
+    int64_t q_batch, q_token, q_head, prefix_token, prefix_head, k_batch, k_token, k_head, table_batch;
+    double scale;
+} df11_prefix_attention_args;
+
+/* Device bytes df11_prefix_attention needs as workspace (partial sums of
+ * key ranges); 0 for arguments it refuses. */
+uint64_t df11_prefix_attention_workspace_bytes(const df11_prefix_attention_args *a);
+
+/* workspace: 16-byte aligned, at least that many bytes, not used by other
+ * work until this call's work has finished; its contents need no clearing.
+ * The result does not depend on the run.  Errors: E_ARG (null or misaligned
+ * pointer -- 16 bytes for q, k, v and out, strides multiples of 8 -- sizes out of
+ * range, dim not a multiple of 8 or above DF11_MAX_DIM, heads not a
+ * multiple of kv_heads, workspace too small), E_DEVICE. */
+int df11_prefix_attention(const df11_prefix_attention_args *a, void *workspace, uint64_t workspace_bytes,
+                          void *stream);
+
+/* A bounded cache: for each sequence and key head `slots` slots of a key, a
+ * value, the attention weight the slot has gathered and the position of its
+ * token.  Sequence b uses the slots [0, lengths[b]).  A slot whose position
+ * is DF11_NO_TOKEN (or negative) holds none; one whose position is at or past the
+ * sequence's next position (a refused draft) is stale: neither is seen, and
+ * they are the first to be replaced. */
+typedef struct df11_cache {
+    void *k, *v;                  /* [batch, kv_heads, slots, dim] */
+    float *weights;               /* [batch, kv_heads, slots], contiguous */
+    int32_t *positions;           /* [batch, kv_heads, slots], contiguous */
+    const int32_t *lengths;       /* [batch] */
+    int64_t dtype, batch, kv_heads, slots, dim, stride_batch, stride_head, stride_slot;
+} df11_cache;
+
+/* Attention over a bounded cache: query token t of sequence b, at position
+ * pos[b] + t, sees the used slots whose position is at most its own; o as
+ * in df11_prefix_attention.  weights[b, h', s] += the sum of the
+ * probabilities that the query tokens and the heads / kv_heads heads of h'
+ * gave slot s.  Every weight is added by one thread in a fixed order. */
+typedef struct df11_cache_attention_args {
+    const void *q;
+    const int32_t *pos;           /* [batch] */
+    void *out;                    /* [batch, tokens, heads, dim], contiguous */
+    int64_t tokens, heads, q_batch, q_token, q_head;
+    double scale;
+} df11_cache_attention_args;
+
+uint64_t df11_cache_attention_workspace_bytes(const df11_cache *c, const df11_cache_attention_args *a);
+/* Workspace and errors as df11_prefix_attention. */
+int df11_cache_attention(const df11_cache *c, const df11_cache_attention_args *a, void *workspace,
+                         uint64_t workspace_bytes, void *stream);
+
+/* One token into every sequence's cache: k_new, v_new [batch, kv_heads, dim]
+ * (strides new_batch, new_head) at position pos[b], with weight 0.  Each key
+ * head takes the slot lengths[b] while that is below `slots`; then the first
+ * stale slot; then, of the slots whose position is at most pos[b] - recent
+ * (the `recent` latest positions, the new one among them, are kept), the
+ * one of least weight, the lowest of equals (a NaN weight counts as less
+ * than any); and if there is none, the slot of the lowest position.  A
+ * sequence with pos[b] < 0 takes no token.  out_slots [batch, kv_heads]: the slot taken, or
+ * -1.  out_lengths [batch]: min(lengths[b] + 1, slots), lengths[b] for a
+ * sequence that takes none (lengths itself is not written; out_lengths must
+ * be another array).  Errors: as df11_prefix_attention. */
+int df11_cache_insert(const df11_cache *c, const void *k_new, const void *v_new, int64_t new_batch,
+                      int64_t new_head, const int32_t *pos, int64_t recent, int32_t *out_slots,
+                      int32_t *out_lengths, void *stream);
+
+/* A cache cut down to `budget` slots for each sequence and key head, into
+ * another cache `out` (of out->slots >= budget slots, same batch, heads,
+ * dim and type; out->lengths is not used).  With pos[b] the sequence's next
+ * position: stale slots are dropped; of the others the `recent` latest
+ * positions are kept, then the greatest weights, the lowest slot of equals
+ * (NaN as above), `budget` in all; they keep their slot order.  kept [batch, kv_heads, out->slots]: the
+ * slots of `c` that were kept, -1 behind them.  Slots of `out` behind the
+ * kept ones are zero with weight 0 and position DF11_NO_TOKEN.  out_lengths[b] =
+ * min(lengths[b], budget).  Errors: as df11_prefix_attention, and E_ARG for
+ * recent > budget or budget > out->slots. */
+int df11_cache_compact(const df11_cache *c, const int32_t *pos, int64_t budget, int64_t recent,
+                       const df11_cache *out, int32_t *kept, int32_t *out_lengths, void *stream);
+
+/* Verification of drafted tokens by rejection sampling, which leaves the
+ * emitted tokens distributed as the target model's.  For each sequence the
+ * drafts i = 0, 1, ... are taken in order while u_i * q_i(d_i) < p_i(d_i)
+ * (p the target's probabilities, q the drafter's; the product exact).  At
+ * the first one refused a token is drawn from max(p_i - q_i, 0), or from p
+ * behind the last draft when all are taken, by the last uniform u: the
+ * first token whose running sum exceeds u times the whole sum.  The sums are
+ * taken over whole multiples of 2^-40 (each probability clamped to [0, 1],
+ * NaN as 0, and cut to such a multiple), so no order of summation changes
+ * them.  Where max(p - q, 0) is zero everywhere p is used; where that is zero
+ * too the drawn token is -1. */
+typedef struct df11_verify_args {
+    const void *draft_tokens;     /* [batch, drafts], int32 or int64 (token_bytes 4 or 8), contiguous */
+    const int32_t *counts;        /* [batch] drafts of each sequence (clamped to [0, drafts]), or NULL: all */
+    const void *target_probs;     /* [batch, drafts + 1, vocab]; sequence b's row behind its last draft is counts[b] */
+    const void *draft_probs;      /* [batch, drafts, vocab], or NULL: the drafter is certain, q(d) = 1 */
+    const float *uniforms;        /* [batch, drafts + 1] in [0, 1), contiguous; the last one draws */
+    void *tokens;                 /* [batch, drafts + 1]: the drafts taken, the drawn token, then -1 */
+    int32_t *accepted;            /* [batch] drafts taken */
+    int64_t dtype, token_bytes, batch, drafts, vocab;
+    int64_t target_batch, target_row, draft_batch, draft_row;
+} df11_verify_args;
+
+uint64_t df11_verify_drafts_workspace_bytes(const df11_verify_args *a);
+/* A drafted token outside [0, vocab) is refused (p = q = 0 there).  vocab at
+ * most 2^22, drafts at most 1024.  Workspace as df11_prefix_attention.  Errors: E_ARG, E_DEVICE. */
+int df11_verify_drafts(const df11_verify_args *a, void *workspace, uint64_t workspace_bytes, void *stream);
+
 /* ---------------------------------------------------------------- utilities */
 const char *df11_status_string(int status);
 const char *df11_last_error(void);
