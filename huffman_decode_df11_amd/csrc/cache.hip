@@ -46,10 +46,12 @@ __global__ void __launch_bounds__(kInsertThreads) insert_kernel(const Cache c, c
     int slot = n;
     if (n == c.slots) {
         uint64_t best = ~0ull;
+#pragma unroll 8
         for (int i = threadIdx.x; i < n; i += kInsertThreads) {
             const int32_t at = c.positions[row + i];
+            const float w = c.weights[row + i];   // read with the position, not behind it
             const uint64_t kind = at >= p || at < 0 ? 0 : (int64_t)at <= (int64_t)p - recent ? 1 : 2;
-            const uint32_t value = kind == 0 ? 0 : kind == 1 ? order_of(c.weights[row + i]) : (uint32_t)at ^ 0x80000000u;
+            const uint32_t value = kind == 0 ? 0 : kind == 1 ? order_of(w) : (uint32_t)at ^ 0x80000000u;
             best = min(best, kind << 62 | (uint64_t)value << 30 | (uint32_t)i);
         }
         for (int d = 32; d; d >>= 1) best = min(best, (uint64_t)__shfl_xor((unsigned long long)best, d));
@@ -72,90 +74,125 @@ __global__ void __launch_bounds__(kInsertThreads) insert_kernel(const Cache c, c
 }
 
 constexpr int kSelectThreads = 1024;
+constexpr int kSelectWaves = kSelectThreads / 64;
 
-// What a slot is worth keeping: 0 not at all (stale, or without a token), then its
-// weight's order, the recent window above all.
-__device__ __forceinline__ uint32_t worth(const Cache &c, int64_t row, int i, int32_t pos, int64_t recent)
+// What a slot is worth keeping: 0 not at all (stale, or without a token),
+// then its weight's order, the recent window above all.
+__device__ __forceinline__ uint32_t worth(int32_t at, float w, int32_t pos, int64_t recent)
 {
-    const int32_t at = c.positions[row + i];
     if (at >= pos || at < 0) return 0;
     if ((int64_t)at >= (int64_t)pos - recent) return 0xffffffffu;
-    return max(1u, order_of(c.weights[row + i]));
+    return max(1u, order_of(w));
 }
 
-// Sum over a workgroup of the counts before this thread's, and of all.
-__device__ __forceinline__ void scan2(uint32_t x, uint32_t *part, uint32_t &before, uint32_t &total)
-{
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t s = x;
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t y = __shfl_up(s, d);
-        if (lane >= d) s += y;
-    }
-    __syncthreads();
-    if (lane == 63) part[wave] = s;
-    __syncthreads();
-    before = s - x;
-    total = 0;
-    for (int w = 0; w < kSelectThreads / 64; w++) {
-        if (w < wave) before += part[w];
-        total += part[w];
-    }
-}
-
-// One workgroup for each sequence and key head: the worth of the last slot
-// that stays, by four passes over its bytes, then the kept slots in order.
+// One workgroup for each sequence and key head.  A wave holds the worths of
+// 64 * N slots in a row, N to a lane, in registers; the worth of the last
+// slot that stays is found two bits at a time by counting (a comparison's
+// mask and its population count: no histogram, whose few busy bins would
+// serialise), then each wave writes its kept slots behind those of the waves
+// before it.  A cache of more than 1024 N slots is taken in rounds, whose
+// worths are computed again for each count.
+template <int N>
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const Cache c, const int32_t *pos, int32_t budget,
                                                                 int64_t recent, const Cache out, int32_t *kept,
                                                                 int32_t *out_lengths)
 {
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t part[kSelectThreads / 64];
-    __shared__ uint32_t chosen[2];
-    const int bh = blockIdx.x, b = bh / c.kv_heads;
+    constexpr int kRound = kSelectThreads * N;
+    __shared__ uint32_t counts[16][3];
+    __shared__ uint32_t waves[2][kSelectWaves][2];
+    __shared__ uint32_t above;
+    const int bh = blockIdx.x, b = bh / c.kv_heads, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = max(0, min(c.lengths[b], c.slots)), p = pos[b];
     const int64_t row = (int64_t)bh * c.slots, out_row = (int64_t)bh * out.slots;
+    const int rounds = (n + kRound - 1) / kRound;
     if (threadIdx.x == 0 && bh % c.kv_heads == 0) out_lengths[b] = min(n, budget);
+    if (threadIdx.x < 48) counts[threadIdx.x / 3][threadIdx.x % 3] = 0;
+    if (threadIdx.x == 0) above = 0;
+    __syncthreads();
 
-    // the least worth that stays, and how many of just that worth stay
-    uint32_t limit = 0, want = budget;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (threadIdx.x < 256) hist[threadIdx.x] = 0;
-        __syncthreads();
-        for (int i = threadIdx.x; i < n; i += kSelectThreads) {
-            const uint32_t w = worth(c, row, i, p, recent);
-            if (shift == 24 || w >> (shift + 8) == limit >> (shift + 8)) atomicAdd(&hist[w >> shift & 255], 1u);
+    uint32_t w[N];
+    const auto load = [&](int round) {
+        const int first = round * kRound + wave * 64 * N + lane;
+        int32_t at[N];
+        float x[N];
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            const int i = min(first + 64 * j, n - 1);
+            at[j] = c.positions[row + i], x[j] = c.weights[row + i];
         }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            // from the top: the byte at which `want` slots are reached (0, if they are not)
-            uint32_t left = want, byte = 255;
-            while (byte && hist[byte] < left) left -= hist[byte--];
-            chosen[0] = limit | byte << shift;
-            chosen[1] = left;
+#pragma unroll
+        for (int j = 0; j < N; j++) w[j] = first + 64 * j < n ? worth(at[j], x[j], p, recent) : 0;
+    };
+    if (rounds == 1) load(0);
+
+    // the greatest worth that at least `budget` slots reach
+    uint32_t limit = 0;
+    for (int pass = 0; pass < 16; pass++) {
+        const uint32_t bit = 1u << (30 - 2 * pass);
+        uint32_t many[3] = {0, 0, 0};
+        for (int round = 0; round < rounds; round++) {
+            if (rounds > 1) load(round);
+#pragma unroll
+            for (int j = 0; j < N; j++)
+#pragma unroll
+                for (int k = 0; k < 3; k++) many[k] += __popcll(__ballot(w[j] >= limit + (k + 1) * bit));
         }
+        if (lane == 0)
+#pragma unroll
+            for (int k = 0; k < 3; k++) atomicAdd(&counts[pass][k], many[k]);
         __syncthreads();
-        limit = chosen[0], want = chosen[1];
+        uint32_t up = 0;
+#pragma unroll
+        for (int k = 0; k < 3; k++) up += counts[pass][k] >= (uint32_t)budget;
+        limit += up * bit;
     }
-    // slots worth nothing never stay
-    if (limit == 0) limit = 1, want = n;
-    uint32_t done = 0, equal = 0;
-    for (int i0 = 0; i0 < n; i0 += kSelectThreads) {
-        const int i = i0 + threadIdx.x;
-        const uint32_t w = i < n ? worth(c, row, i, p, recent) : 0;
-        uint32_t before, total;
-        scan2(w == limit, part, before, total);
-        const bool stays = w > limit || (w == limit && equal + before < want);
-        equal += total;
-        scan2(stays, part, before, total);
-        if (stays) {
-            const int64_t to = out_row + done + before;
-            kept[to] = i;
-            out.weights[to] = c.weights[row + i];
-            out.positions[to] = c.positions[row + i];
-        }
-        done += total;
+    if (limit == 0) limit = 1;   // fewer than `budget` slots are worth anything: all of those
+
+    uint32_t g = 0;
+    for (int round = 0; round < rounds; round++) {
+        if (rounds > 1) load(round);
+#pragma unroll
+        for (int j = 0; j < N; j++) g += __popcll(__ballot(w[j] > limit));
     }
+    if (lane == 0) atomicAdd(&above, g);
+    __syncthreads();
+    // of the slots worth just `limit` the first `want` stay
+    const uint32_t want = budget - above;
+    const uint64_t before = (1ull << lane) - 1;
+    uint32_t more = 0, equal = 0;   // slots worth more and just `limit` in the rounds so far
+    for (int round = 0; round < rounds; round++) {
+        if (rounds > 1) load(round);
+        uint32_t mine[2] = {0, 0};
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            mine[0] += __popcll(__ballot(w[j] > limit));
+            mine[1] += __popcll(__ballot(w[j] == limit));
+        }
+        if (lane < 2) waves[round & 1][wave][lane] = mine[lane];
+        __syncthreads();
+        uint32_t m = more, e = equal;
+#pragma unroll
+        for (int v = 0; v < kSelectWaves; v++) {
+            const uint32_t vm = waves[round & 1][v][0], ve = waves[round & 1][v][1];
+            m += v < wave ? vm : 0, e += v < wave ? ve : 0;
+            more += vm, equal += ve;
+        }
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            const uint64_t over = __ballot(w[j] > limit), same = __ballot(w[j] == limit);
+            const uint32_t rank = e + __popcll(same & before);
+            if (w[j] > limit || (w[j] == limit && rank < want)) {
+                const int i = round * kRound + (wave * N + j) * 64 + lane;
+                const int64_t to = out_row + m + __popcll(over & before) + min(rank, want);
+                kept[to] = i;
+                out.weights[to] = c.weights[row + i];
+                out.positions[to] = c.positions[row + i];
+            }
+            m += __popcll(over), e += __popcll(same);
+        }
+    }
+    const int done = more + min(equal, want);
     for (int i = done + threadIdx.x; i < out.slots; i += kSelectThreads) {
         kept[out_row + i] = -1;
         out.weights[out_row + i] = 0.0f;
@@ -250,8 +287,11 @@ extern "C" int df11_cache_compact(const df11_cache *cache, const int32_t *pos, i
     if (c.slots && (out.k == c.k || out.v == c.v || out.weights == c.weights || out.positions == c.positions))
         return df11::fail(DF11_E_ARG, "%s: a cache is not cut down in place", who);
     hipStream_t st = (hipStream_t)stream;
-    hipLaunchKernelGGL(select_kernel, dim3(c.batch * c.kv_heads), dim3(kSelectThreads), 0, st, c, pos, (int32_t)budget,
-                       recent, out, kept, out_lengths);
+    const dim3 heads(c.batch * c.kv_heads), threads(kSelectThreads);
+    if (c.slots <= 8 * kSelectThreads)
+        hipLaunchKernelGGL(select_kernel<8>, heads, threads, 0, st, c, pos, (int32_t)budget, recent, out, kept, out_lengths);
+    else
+        hipLaunchKernelGGL(select_kernel<32>, heads, threads, 0, st, c, pos, (int32_t)budget, recent, out, kept, out_lengths);
     hipLaunchKernelGGL(move_kernel, dim3((out.slots + 15) / 16, c.batch * c.kv_heads), dim3(256), 0, st, c, out, kept);
     return launched(who);
 }

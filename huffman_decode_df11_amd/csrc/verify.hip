@@ -26,9 +26,13 @@ struct Args {
     int32_t *accepted;
     int32_t token_bytes, batch, drafts, vocab;
     int64_t target_batch, target_row, draft_batch, draft_row;
+    int32_t parts;
+    u64 *sums;   // [batch][parts][2]
 };
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 256;
+constexpr int kRun = 8;                          // tokens a thread holds in the last search
+constexpr int kPiece = kThreads * kRun * 4;      // tokens of a part: 2^13, so that a part's sum is below 2^53
 
 struct F32 {
     typedef float type;
@@ -46,12 +50,9 @@ struct HF {
     static __device__ __forceinline__ float value(uint16_t x) { return (float)__builtin_bit_cast(_Float16, x); }
 };
 
-// p in whole multiples of 2^-40, of p clamped to [0, 1]; NaN is 0
-__device__ __forceinline__ u64 whole(float p)
-{
-    p = p > 0.0f ? fminf(p, 1.0f) : 0.0f;
-    return (u64)(p * 1099511627776.0f);
-}
+// p in whole multiples of 2^-40, of p clamped to [0, 1]; NaN is 0.  A
+// double holds such numbers, and their sums below 2^53, exactly.
+__device__ __forceinline__ double whole(float p) { return __builtin_trunc((double)fminf(fmaxf(p, 0.0f), 1.0f) * 0x1p40); }
 
 __device__ __forceinline__ int64_t token(const void *t, int bytes, int64_t i)
 {
@@ -64,8 +65,14 @@ __device__ __forceinline__ void put(void *t, int bytes, int64_t i, int64_t v)
     else ((int32_t *)t)[i] = (int32_t)v;
 }
 
-// Sum over the workgroup of the values before this thread's, and of all.
-__device__ __forceinline__ void scan(u64 x, u64 *part, u64 &before, u64 &total)
+__device__ __forceinline__ u64 wave_sum(u64 x)
+{
+    for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
+    return x;
+}
+
+// Sum over the workgroup of the values before this thread's.
+__device__ __forceinline__ u64 sum_before(u64 x, u64 *part)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     u64 s = x;
@@ -76,35 +83,29 @@ __device__ __forceinline__ void scan(u64 x, u64 *part, u64 &before, u64 &total)
     __syncthreads();
     if (lane == 63) part[wave] = s;
     __syncthreads();
-    before = s - x;
-    total = 0;
-    for (int w = 0; w < kThreads / 64; w++) {
-        if (w < wave) before += part[w];
-        total += part[w];
-    }
+    s -= x;
+    for (int w = 0; w < wave; w++) s += part[w];
+    return s;
 }
 
-// The weight of token i where the row of p is `p` and that of q is `q`
-// (null: certain of token `sure`, -1 none).
+// The rows that a sequence's drawn token comes from: p's and, if a draft was
+// refused, q's (null for a certain drafter, whose token is `sure`).
 template <class T>
-__device__ __forceinline__ u64 weight(const typename T::type *p, const typename T::type *q, int64_t sure, int i, bool rest)
-{
-    const u64 x = whole(T::value(p[i]));
-    if (!rest) return x;
-    const u64 y = q ? whole(T::value(q[i])) : i == sure ? 1ull << 40 : 0;
-    return x > y ? x - y : 0;
-}
+struct Rows {
+    const typename T::type *p, *q;
+    int64_t sure;
+    bool rest;
+    // what token i adds to the sum of max(p - q, 0), x its share of p
+    __device__ __forceinline__ double left(double x, double y) const { return fmax(x - y, 0.0); }
+    __device__ __forceinline__ double refused(int64_t i) const { return i == sure ? 0x1p40 : 0.0; }
+};
 
-// One workgroup for each sequence; each thread has a run of the vocabulary.
+// The number of drafts taken: where the first is refused.
 template <class T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const Args a)
+__device__ __forceinline__ int drafts_taken(const Args &a, int b, int count, int *lds)
 {
     typedef typename T::type type;
-    __shared__ u64 part[kThreads / 64];
-    __shared__ int first_refused, drawn;
-    const int b = blockIdx.x;
-    const int count = a.counts ? max(0, min(a.counts[b], a.drafts)) : a.drafts;
-    if (threadIdx.x == 0) first_refused = count, drawn = -1;
+    if (threadIdx.x == 0) *lds = count;
     __syncthreads();
     for (int i = threadIdx.x; i < count; i += kThreads) {
         const int64_t d = token(a.draft_tokens, a.token_bytes, (int64_t)b * a.drafts + i);
@@ -114,44 +115,171 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Args a)
             q = a.draft ? (double)T::value(((const type *)a.draft)[b * a.draft_batch + i * a.draft_row + d]) : 1.0;
         }
         const double u = a.uniforms[(int64_t)b * (a.drafts + 1) + i];
-        if (!(u * q < p)) atomicMin(&first_refused, i);
+        if (!(u * q < p)) atomicMin(lds, i);   // u has 24 bits and q at most 24: the product is exact
     }
     __syncthreads();
-    const int n = first_refused;
-    const type *p = (const type *)a.target + b * a.target_batch + n * a.target_row;
-    const type *q = a.draft && n < count ? (const type *)a.draft + b * a.draft_batch + n * a.draft_row : nullptr;
-    const int64_t sure = n < count ? token(a.draft_tokens, a.token_bytes, (int64_t)b * a.drafts + n) : -1;
-    const int run = (a.vocab + kThreads - 1) / kThreads;
-    const int i0 = min(a.vocab, (int)threadIdx.x * run), i1 = min(a.vocab, i0 + run);
-    bool rest = n < count;
-    u64 before, total, mine;
-    for (;;) {
-        mine = 0;
-        for (int i = i0; i < i1; i++) mine += weight<T>(p, q, sure, i, rest);
-        scan(mine, part, before, total);
-        if (total || !rest) break;
-        rest = false;
+    return *lds;
+}
+
+template <class T>
+__device__ __forceinline__ Rows<T> rows_of(const Args &a, int b, int count, int n)
+{
+    typedef typename T::type type;
+    return Rows<T>{(const type *)a.target + b * a.target_batch + n * a.target_row,
+                   a.draft && n < count ? (const type *)a.draft + b * a.draft_batch + n * a.draft_row : nullptr,
+                   n < count && !a.draft ? token(a.draft_tokens, a.token_bytes, (int64_t)b * a.drafts + n) : -1,
+                   n < count};
+}
+
+// The sums over tokens [i0, i1) of max(p - q, 0) (of p behind the last
+// draft) and of p, complete in thread 0.  16 bytes of a row a thread at a
+// time, at any alignment.
+template <class T>
+__device__ __forceinline__ void part_sums(const Rows<T> &r, int i0, int i1, u64 *lds, u64 &rest, u64 &all)
+{
+    typedef typename T::type type;
+    constexpr int V = 16 / sizeof(type);
+    struct Vec { type x[V]; };
+    double sr = 0.0, sp = 0.0;
+    const int whole_vecs = (i1 - i0) / V;
+#pragma unroll 4
+    for (int k = threadIdx.x; k < whole_vecs; k += kThreads) {
+        const int i = i0 + k * V;
+        Vec p, q;
+        __builtin_memcpy(&p, r.p + i, 16);
+        if (r.q) __builtin_memcpy(&q, r.q + i, 16);
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+            const double x = whole(T::value(p.x[j]));
+            sp += x;
+            if (r.rest) sr += r.left(x, r.q ? whole(T::value(q.x[j])) : r.refused(i + j));
+        }
     }
-    // the token whose share of the sum holds u * total
-    const u64 u = (u64)(fminf(fmaxf(a.uniforms[(int64_t)b * (a.drafts + 1) + a.drafts], 0.0f), 0.99999994f) * 16777216.0f);
-    const u64 goal = __umul64hi(u << 40, total);
-    if (total && before <= goal && goal < before + mine) {
-        u64 s = before;
-        for (int i = i0; i < i1; i++) {
-            s += weight<T>(p, q, sure, i, rest);
-            if (goal < s) {
-                drawn = i;
-                break;
-            }
+    const int i = i0 + whole_vecs * V + threadIdx.x;
+    if (i < i1) {
+        const double x = whole(T::value(r.p[i]));
+        sp += x;
+        if (r.rest) sr += r.left(x, r.q ? whole(T::value(r.q[i])) : r.refused(i));
+    }
+    const u64 wr = wave_sum((u64)sr), wp = wave_sum((u64)sp);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __syncthreads();
+    if (lane == 0) lds[wave] = wr, lds[kThreads / 64 + wave] = wp;
+    __syncthreads();
+    rest = all = 0;
+    for (int w = 0; w < kThreads / 64; w++) rest += lds[w], all += lds[kThreads / 64 + w];
+    if (!r.rest) rest = all;
+}
+
+// Parts of the vocabulary: each writes its two sums.
+template <class T>
+__global__ void __launch_bounds__(kThreads) part_kernel(const Args a)
+{
+    __shared__ u64 lds[2 * kThreads / 64];
+    __shared__ int first_refused;
+    const int part = blockIdx.x, b = blockIdx.y;
+    const int count = a.counts ? max(0, min(a.counts[b], a.drafts)) : a.drafts;
+    const int n = drafts_taken<T>(a, b, count, &first_refused);
+    u64 rest, all;
+    part_sums<T>(rows_of<T>(a, b, count, n), part * kPiece, min(a.vocab, (part + 1) * kPiece), lds, rest, all);
+    if (threadIdx.x == 0) {
+        u64 *to = a.sums + ((int64_t)b * a.parts + part) * 2;
+        to[0] = rest, to[1] = all;
+    }
+}
+
+// One workgroup for each sequence finds the part that holds u times the
+// whole sum, in it the thread's run, and in that the token.  A vocabulary of
+// one part is summed here too.
+template <class T>
+__global__ void __launch_bounds__(kThreads) draw_kernel(const Args a)
+{
+    __shared__ u64 lds[2 * kThreads / 64];
+    __shared__ u64 before_part;
+    __shared__ int first_refused, chosen, drawn;
+    const int b = blockIdx.x;
+    const int count = a.counts ? max(0, min(a.counts[b], a.drafts)) : a.drafts;
+    const int n = drafts_taken<T>(a, b, count, &first_refused);
+    Rows<T> r = rows_of<T>(a, b, count, n);
+    const float last = a.uniforms[(int64_t)b * (a.drafts + 1) + a.drafts];
+    const u64 u = (u64)(fminf(fmaxf(last, 0.0f), 0.99999994f) * 16777216.0f);
+    u64 rest = 0, all = 0;
+    if (threadIdx.x == 0) drawn = -1, chosen = 0, before_part = 0;
+    if (a.parts == 1) {
+        part_sums<T>(r, 0, a.vocab, lds, rest, all);
+    } else {
+        u64 mine[2] = {0, 0};
+        for (int i = threadIdx.x; i < a.parts; i += kThreads) {
+            const u64 *from = a.sums + ((int64_t)b * a.parts + i) * 2;
+            mine[0] += from[0], mine[1] += from[1];
+        }
+        mine[0] = wave_sum(mine[0]), mine[1] = wave_sum(mine[1]);
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        if (lane == 0) lds[wave] = mine[0], lds[kThreads / 64 + wave] = mine[1];
+        __syncthreads();
+        for (int w = 0; w < kThreads / 64; w++) rest += lds[w], all += lds[kThreads / 64 + w];
+    }
+    if (!rest) r.rest = false;   // nothing is left of p - q: p itself
+    const u64 total = rest ? rest : all;
+    const u64 goal = __umul64hi(u << 40, total);   // floor(u * total / 2^24), below total
+    if (a.parts > 1) {
+        // at most 512 parts: two for each thread, in order
+        u64 x[2];
+        for (int j = 0; j < 2; j++) {
+            const int i = 2 * threadIdx.x + j;
+            x[j] = i < a.parts ? a.sums[((int64_t)b * a.parts + i) * 2 + (rest ? 0 : 1)] : 0;
+        }
+        u64 s = sum_before(x[0] + x[1], lds);
+        for (int j = 0; j < 2; j++) {
+            if (s <= goal && goal < s + x[j]) chosen = 2 * threadIdx.x + j, before_part = s;
+            s += x[j];
         }
     }
     __syncthreads();
+    u64 start = before_part;
+    const int part = chosen;
+    // the part in rounds of kRun tokens a thread
+    for (int i0 = part * kPiece; i0 < min(a.vocab, (part + 1) * kPiece); i0 += kThreads * kRun) {
+        const int first = i0 + threadIdx.x * kRun;
+        double x[kRun], sum = 0.0;
+#pragma unroll
+        for (int j = 0; j < kRun; j++) {
+            const int i = first + j;
+            x[j] = 0.0;
+            if (i < a.vocab) {
+                x[j] = whole(T::value(r.p[i]));
+                if (r.rest) x[j] = r.left(x[j], r.q ? whole(T::value(r.q[i])) : r.refused(i));
+            }
+            sum += x[j];
+        }
+        u64 s = start + sum_before((u64)sum, lds);
+        if (s <= goal && goal < s + (u64)sum) {
+#pragma unroll
+            for (int j = 0; j < kRun; j++) {
+                if (s <= goal && goal < s + (u64)x[j]) drawn = first + j;
+                s += (u64)x[j];
+            }
+        }
+        for (int w = 0; w < kThreads / 64; w++) start += lds[w];
+        __syncthreads();
+        if (drawn >= 0) break;
+    }
     for (int i = threadIdx.x; i <= a.drafts; i += kThreads) {
         const int64_t at = (int64_t)b * (a.drafts + 1) + i;
         put(a.tokens, a.token_bytes, at,
             i < n ? token(a.draft_tokens, a.token_bytes, (int64_t)b * a.drafts + i) : i == n ? drawn : -1);
     }
     if (threadIdx.x == 0) a.accepted[b] = n;
+}
+
+template <class T>
+int launch(const Args &a, hipStream_t st)
+{
+    if (a.parts > 1) hipLaunchKernelGGL(part_kernel<T>, dim3(a.parts, a.batch), dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL(draw_kernel<T>, dim3(a.batch), dim3(kThreads), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return df11::fail(DF11_E_DEVICE, "df11_verify_drafts launch: %s", hipGetErrorString(e));
+    return DF11_OK;
 }
 
 int check(const df11_verify_args *p, Args &a)
@@ -162,14 +290,15 @@ int check(const df11_verify_args *p, Args &a)
         return df11::fail(DF11_E_ARG, "%s: dtype must be bf16, fp16 or fp32", who);
     if (p->token_bytes != 4 && p->token_bytes != 8)
         return df11::fail(DF11_E_ARG, "%s: tokens must be int32 or int64", who);
-    if (p->batch < 0 || p->batch > (1 << 20) || p->drafts < 0 || p->drafts > 1024 || p->vocab < 1 ||
+    if (p->batch < 0 || p->batch > 65535 || p->drafts < 0 || p->drafts > 1024 || p->vocab < 1 ||
         p->vocab > (1 << 22))
         return df11::fail(DF11_E_ARG, "%s: batch, drafts or vocab out of range", who);
     if (p->target_batch < 0 || p->target_row < 0 || p->draft_batch < 0 || p->draft_row < 0)
         return df11::fail(DF11_E_ARG, "%s: negative stride", who);
     a = Args{p->draft_tokens, p->counts, (const uint8_t *)p->target_probs, (const uint8_t *)p->draft_probs, p->uniforms,
              p->tokens, p->accepted, (int32_t)p->token_bytes, (int32_t)p->batch, (int32_t)p->drafts, (int32_t)p->vocab,
-             p->target_batch, p->target_row, p->draft_batch, p->draft_row};
+             p->target_batch, p->target_row, p->draft_batch, p->draft_row,
+             (int32_t)((p->vocab + kPiece - 1) / kPiece), nullptr};
     return DF11_OK;
 }
 
@@ -177,8 +306,8 @@ int check(const df11_verify_args *p, Args &a)
 
 extern "C" uint64_t df11_verify_drafts_workspace_bytes(const df11_verify_args *p)
 {
-    (void)p;
-    return 0;
+    Args a;
+    return check(p, a) || a.parts == 1 ? 0 : 16ull * a.batch * a.parts;
 }
 
 extern "C" int df11_verify_drafts(const df11_verify_args *p, void *workspace, uint64_t workspace_bytes, void *stream)
@@ -192,11 +321,11 @@ extern "C" int df11_verify_drafts(const df11_verify_args *p, void *workspace, ui
     if (!a.target || ((uintptr_t)a.target & mask) || ((uintptr_t)a.draft & mask) || !a.uniforms || !a.tokens ||
         !a.accepted || (a.drafts && !a.draft_tokens))
         return df11::fail(DF11_E_ARG, "%s: null or misaligned pointer", who);
+    const uint64_t need = a.parts > 1 ? 16ull * a.batch * a.parts : 0;
+    if (workspace_bytes < need || (need && !aligned16(workspace)))
+        return df11::fail(DF11_E_ARG, "%s: the workspace must be 16-byte aligned and hold %llu bytes", who,
+                          (unsigned long long)need);
+    a.sums = (u64 *)workspace;
     hipStream_t st = (hipStream_t)stream;
-    if (p->dtype == DF11_FP32) hipLaunchKernelGGL(verify_kernel<F32>, dim3(a.batch), dim3(kThreads), 0, st, a);
-    else if (p->dtype == DF11_BF16) hipLaunchKernelGGL(verify_kernel<BF>, dim3(a.batch), dim3(kThreads), 0, st, a);
-    else hipLaunchKernelGGL(verify_kernel<HF>, dim3(a.batch), dim3(kThreads), 0, st, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return df11::fail(DF11_E_DEVICE, "%s launch: %s", who, hipGetErrorString(e));
-    return DF11_OK;
+    return p->dtype == DF11_FP32 ? launch<F32>(a, st) : p->dtype == DF11_BF16 ? launch<BF>(a, st) : launch<HF>(a, st);
 }

@@ -37,72 +37,70 @@ _CACHE_ARGS = struct.Struct("8qd")
 _VERIFY_ARGS = struct.Struct("16q")
 
 
-def _refuse(cond: bool, text: str) -> None:
-    if cond:
-        raise ValueError(text)
-
-
-def _on(name: str, t, dtype, device, shape=None) -> int:
-    """The address of a contiguous tensor of this type, device and shape."""
+def _same(name: str, t, dtype, device) -> None:
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    _refuse(t.device != device, "%s is on %s, the other operands on %s" % (name, t.device, device))
-    _refuse(shape is not None and tuple(t.shape) != shape, "%s has shape %s, not %s" % (name, tuple(t.shape), shape))
-    _refuse(not t.is_contiguous(), "%s must be contiguous" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, the other operands on %s" % (name, t.device, device))
+
+
+def _flat(name: str, t, dtype, device, shape) -> int:
+    """The address of a contiguous tensor of this type, device and shape."""
+    if t.dtype != dtype or t.device != device:
+        _same(name, t, dtype, device)
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), shape))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
     return t.data_ptr()
 
 
-def _rows(name: str, t, like, shape):
-    """The strides of a tensor of rows (last axis contiguous) like `like`."""
-    if t.dtype != like.dtype:
-        raise TypeError("%s must be %s, got %s" % (name, like.dtype, t.dtype))
-    _refuse(t.device != like.device, "%s is on %s, the other operands on %s" % (name, t.device, like.device))
-    _refuse(tuple(t.shape) != shape, "%s has shape %s, not %s" % (name, tuple(t.shape), shape))
+def _rows(name: str, t, dtype, device, shape):
+    """The strides of a tensor of rows, its last axis contiguous."""
+    if t.dtype != dtype or t.device != device:
+        _same(name, t, dtype, device)
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), shape))
     s = t.stride()
     if 1 in shape:   # the stride of an axis of one is never used
         s = tuple(0 if n == 1 else x for n, x in zip(shape, s))
-    _refuse(s[-1] != 1 and shape[-1] > 1, "the last axis of %s must be contiguous" % name)
+    if s[-1] != 1 and shape[-1] > 1:
+        raise ValueError("the last axis of %s must be contiguous" % name)
     return s
 
 
-def _operand(name: str, t, table=_DTYPES) -> int:
-    _refuse(not t.is_cuda, "%s must be on the GPU" % name)
+def _pair(names: str, a, b, dtype, device, shape):
+    """The strides of keys and values, which share them."""
+    s = _rows(names[:names.index(" ")], a, dtype, device, shape)
+    if _rows(names[names.rindex(" ") + 1:], b, dtype, device, shape) != s:
+        raise ValueError("%s must have the same strides" % names)
+    return s
+
+
+def _code(name: str, t, table) -> int:
+    if not t.is_cuda:
+        raise ValueError("%s must be on the GPU" % name)
     code = table.get(t.dtype)
     if code is None:
         raise TypeError("%s must be one of %s, got %s" % (name, ", ".join(str(d) for d in table), t.dtype))
     return code
 
 
-class _Work:
-    """The device and stream of a call, for its allocations and launches."""
-
-    def __init__(self, device, stream):
-        self.device = device
-        self.guard = None
-        if device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-        self.stream = stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        if self.stream is None:
-            self.ctx, self.handle = None, torch.cuda.current_stream().cuda_stream
-        else:
-            self.ctx, self.handle = torch.cuda.stream(self.stream), self.stream.cuda_stream
-            self.ctx.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+def _here(device, stream) -> bool:
+    """Whether a call can go ahead on the current device's current stream."""
+    return stream is None and device.index == torch.cuda.current_device()
 
 
-def _workspace(nbytes: int, device):
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+def _there(device, stream):
+    """The context in which a call's device and stream are the current ones
+    (its outputs and workspaces belong to that stream)."""
+    return torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
+
+
+# The current stream's handle without the Stream object around it (0.1 of
+# the 2 us that torch.cuda.current_stream takes, of some 10 for a call).
+_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def prefix_attention(q, prefix_k, prefix_v, k, v, lengths, *, block_table=None, scale: Optional[float] = None,
@@ -119,39 +117,46 @@ def prefix_attention(q, prefix_k, prefix_v, k, v, lengths, *, block_table=None, 
     is 1 / sqrt(D) when None.  Returns out [B, T, Hq, D], and with
     return_lse also lse [B, T, Hq] float32.  A row that sees no position is
     zero (lse -inf)."""
-    code = _operand("q", q)
-    _refuse(q.dim() != 4, "q must be [B, T, Hq, D]")
-    B, T, Hq, D = q.shape
-    _refuse(prefix_k.dim() != 3 or k.dim() != 4, "prefix_k must be [P, Hkv, D] and k [B, S, Hkv, D] or pages")
-    P, Hkv = prefix_k.shape[:2]
-    device = q.device
-    sq = _rows("q", q, q, (B, T, Hq, D))
-    sp = _rows("prefix_k", prefix_k, q, (P, Hkv, D))
-    _refuse(_rows("prefix_v", prefix_v, q, (P, Hkv, D)) != sp, "prefix_k and prefix_v must have the same strides")
+    device, dtype = q.device, q.dtype
+    if not _here(device, stream):
+        with _there(device, stream):
+            return prefix_attention(q, prefix_k, prefix_v, k, v, lengths, block_table=block_table, scale=scale, out=out,
+                                    return_lse=return_lse)
+    code = _code("q", q, _DTYPES)
+    if q.dim() != 4 or prefix_k.dim() != 3 or k.dim() != 4:
+        raise ValueError("q must be [B, T, Hq, D], prefix_k [P, Hkv, D] and k [B, S, Hkv, D] or pages")
+    shape = B, T, Hq, D = q.shape
+    P, Hkv, _ = prefix_k.shape
+    sq = _rows("q", q, dtype, device, shape)
+    sp = _pair("prefix_k and prefix_v", prefix_k, prefix_v, dtype, device, (P, Hkv, D))
     if block_table is None:
         S, page, pages, table, st = k.shape[1], 0, 0, 0, 0
-        sk = _rows("k", k, q, (B, S, Hkv, D))
+        sk = _pair("k and v", k, v, dtype, device, (B, S, Hkv, D))
     else:
         pages, page = k.shape[:2]
-        sk = _rows("k", k, q, (pages, page, Hkv, D))
-        _refuse(block_table.dim() != 2 or block_table.shape[0] != B, "block_table must be [B, pages]")
-        table = _on("block_table", block_table, torch.int32, device)
+        sk = _pair("k and v", k, v, dtype, device, (pages, page, Hkv, D))
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [B, pages]")
         st = block_table.shape[1]
+        table = _flat("block_table", block_table, torch.int32, device, (B, st))
         S = st * page
-    _refuse(_rows("v", v, q, tuple(k.shape)) != sk, "k and v must have the same strides")
-    n = _on("lengths", lengths, torch.int32, device, (B,))
-    with _Work(device, stream) as handle:
-        if out is None:
-            out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=device)
-        o = _on("out", out, q.dtype, device, (B, T, Hq, D))
-        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=device) if return_lse else None
-        args = _PREFIX_ARGS.pack(
-            q.data_ptr(), prefix_k.data_ptr(), prefix_v.data_ptr(), k.data_ptr(), v.data_ptr(), n, table, o,
-            lse.data_ptr() if return_lse else 0, code, B, T, Hq, Hkv, D, P, S, page, pages, sq[0], sq[1], sq[2],
-            sp[0], sp[1], sk[0], sk[1], sk[2], st, D ** -0.5 if scale is None else scale)
-        L = lib()
-        ws = _workspace(L.df11_prefix_attention_workspace_bytes(args), device)
-        check(L.df11_prefix_attention(args, ws.data_ptr(), ws.numel(), handle), "df11_prefix_attention")
+    n = _flat("lengths", lengths, torch.int32, device, (B,))
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=device)
+        o = out.data_ptr()
+    else:
+        o = _flat("out", out, dtype, device, shape)
+    lse = torch.empty((B, T, Hq), dtype=torch.float32, device=device) if return_lse else None
+    args = _PREFIX_ARGS.pack(
+        q.data_ptr(), prefix_k.data_ptr(), prefix_v.data_ptr(), k.data_ptr(), v.data_ptr(), n, table, o,
+        lse.data_ptr() if return_lse else 0, code, B, T, Hq, Hkv, D, P, S, page, pages, sq[0], sq[1], sq[2],
+        sp[0], sp[1], sk[0], sk[1], sk[2], st, D ** -0.5 if scale is None else scale)
+    L = lib()
+    nbytes = L.df11_prefix_attention_workspace_bytes(args)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    rc = L.df11_prefix_attention(args, ws.data_ptr(), nbytes, _stream(device.index))
+    if rc:
+        check(rc, "df11_prefix_attention")
     return (out, lse) if return_lse else out
 
 
@@ -166,17 +171,18 @@ class BoundedCache:
     drafts) are not seen and are replaced first."""
 
     def __init__(self, k, v, weights, positions, lengths):
-        self.code = _operand("k", k)
-        _refuse(k.dim() != 4, "k must be [B, Hkv, slots, D]")
+        self.code = _code("k", k, _DTYPES)
+        if k.dim() != 4:
+            raise ValueError("k must be [B, Hkv, slots, D]")
         shape = B, H, C, D = tuple(k.shape)
-        s = _rows("k", k, k, shape)
-        _refuse(_rows("v", v, k, shape) != s, "k and v must have the same strides")
+        dtype, device = k.dtype, k.device
+        s = _pair("k and v", k, v, dtype, device, shape)
         self.k, self.v, self.weights, self.positions, self.lengths = k, v, weights, positions, lengths
-        self.shape, self.device = shape, k.device
+        self.shape, self.dtype, self.device = shape, dtype, device
         self.args = _CACHE.pack(k.data_ptr(), v.data_ptr(),
-                                _on("weights", weights, torch.float32, k.device, (B, H, C)),
-                                _on("positions", positions, torch.int32, k.device, (B, H, C)),
-                                _on("lengths", lengths, torch.int32, k.device, (B,)),
+                                _flat("weights", weights, torch.float32, device, (B, H, C)),
+                                _flat("positions", positions, torch.int32, device, (B, H, C)),
+                                _flat("lengths", lengths, torch.int32, device, (B,)),
                                 self.code, B, H, C, D, s[0], s[1], s[2])
 
     @classmethod
@@ -198,20 +204,29 @@ def cache_attention(q, cache: BoundedCache, pos, *, scale: Optional[float] = Non
     used slots whose positions are at most that; cache.weights grows by the
     probabilities each slot got, summed over the tokens and the heads that
     share its key head.  Returns out [B, T, Hq, D]."""
-    _refuse(q.dim() != 4, "q must be [B, T, Hq, D]")
-    B, T, Hq, D = q.shape
-    _refuse((B, D) != (cache.shape[0], cache.shape[3]), "q has shape %s, the cache %s" % (tuple(q.shape), cache.shape))
-    device = cache.device
-    sq = _rows("q", q, cache.k, (B, T, Hq, D))
-    p = _on("pos", pos, torch.int32, device, (B,))
-    with _Work(device, stream) as handle:
-        if out is None:
-            out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=device)
-        args = _CACHE_ARGS.pack(q.data_ptr(), p, _on("out", out, q.dtype, device, (B, T, Hq, D)), T, Hq, sq[0], sq[1],
-                                sq[2], D ** -0.5 if scale is None else scale)
-        L = lib()
-        ws = _workspace(L.df11_cache_attention_workspace_bytes(cache.args, args), device)
-        check(L.df11_cache_attention(cache.args, args, ws.data_ptr(), ws.numel(), handle), "df11_cache_attention")
+    device, dtype = cache.device, cache.dtype
+    if not _here(device, stream):
+        with _there(device, stream):
+            return cache_attention(q, cache, pos, scale=scale, out=out)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, T, Hq, D]")
+    shape = B, T, Hq, D = q.shape
+    if B != cache.shape[0] or D != cache.shape[3]:
+        raise ValueError("q has shape %s, the cache %s" % (tuple(shape), cache.shape))
+    sq = _rows("q", q, dtype, device, shape)
+    p = _flat("pos", pos, torch.int32, device, (B,))
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=device)
+        o = out.data_ptr()
+    else:
+        o = _flat("out", out, dtype, device, shape)
+    args = _CACHE_ARGS.pack(q.data_ptr(), p, o, T, Hq, sq[0], sq[1], sq[2], D ** -0.5 if scale is None else scale)
+    L = lib()
+    nbytes = L.df11_cache_attention_workspace_bytes(cache.args, args)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    rc = L.df11_cache_attention(cache.args, args, ws.data_ptr(), nbytes, _stream(device.index))
+    if rc:
+        check(rc, "df11_cache_attention")
     return out
 
 
@@ -223,15 +238,19 @@ def cache_insert(cache: BoundedCache, k_new, v_new, pos, recent: int, *, stream=
     those outside the `recent` latest positions.  Returns the slots taken
     [B, Hkv] (-1: none) and the new lengths [B], both int32; cache.lengths
     is left as it is (set_lengths)."""
+    device, dtype = cache.device, cache.dtype
+    if not _here(device, stream):
+        with _there(device, stream):
+            return cache_insert(cache, k_new, v_new, pos, recent)
     B, H, C, D = cache.shape
-    s = _rows("k_new", k_new, cache.k, (B, H, D))
-    _refuse(_rows("v_new", v_new, cache.k, (B, H, D)) != s, "k_new and v_new must have the same strides")
-    p = _on("pos", pos, torch.int32, cache.device, (B,))
-    with _Work(cache.device, stream) as handle:
-        slots = torch.empty((B, H), dtype=torch.int32, device=cache.device)
-        lengths = torch.empty((B,), dtype=torch.int32, device=cache.device)
-        check(lib().df11_cache_insert(cache.args, k_new.data_ptr(), v_new.data_ptr(), s[0], s[1], p, recent,
-                                      slots.data_ptr(), lengths.data_ptr(), handle), "df11_cache_insert")
+    s = _pair("k_new and v_new", k_new, v_new, dtype, device, (B, H, D))
+    p = _flat("pos", pos, torch.int32, device, (B,))
+    slots = torch.empty((B, H), dtype=torch.int32, device=device)
+    lengths = torch.empty((B,), dtype=torch.int32, device=device)
+    rc = lib().df11_cache_insert(cache.args, k_new.data_ptr(), v_new.data_ptr(), s[0], s[1], p, recent, slots.data_ptr(),
+                                 lengths.data_ptr(), _stream(device.index))
+    if rc:
+        check(rc, "df11_cache_insert")
     return slots, lengths
 
 
@@ -241,19 +260,24 @@ def cache_compact(cache: BoundedCache, pos, budget: int, recent: int, *, slots: 
     before pos[b], then the greatest weights (the lowest slot of equals), in
     slot order.  Returns it and kept [B, Hkv, slots] int32, the slots that
     were kept (-1 behind them)."""
+    device, dtype = cache.device, cache.dtype
+    if not _here(device, stream):
+        with _there(device, stream):
+            return cache_compact(cache, pos, budget, recent, slots=slots)
     B, H, C, D = cache.shape
-    device = cache.device
     slots = budget if slots is None else slots
-    _refuse(slots < 1, "the new cache needs a slot")
-    p = _on("pos", pos, torch.int32, device, (B,))
-    with _Work(device, stream) as handle:
-        kv = torch.empty((2, B, H, slots, D), dtype=cache.k.dtype, device=device)
-        numbers = torch.empty((2, B, H, slots), dtype=torch.int32, device=device)
-        cut = BoundedCache(kv[0], kv[1], torch.empty((B, H, slots), dtype=torch.float32, device=device), numbers[0],
-                           torch.empty((B,), dtype=torch.int32, device=device))
-        check(lib().df11_cache_compact(cache.args, p, budget, recent, cut.args, numbers[1].data_ptr(),
-                                       cut.lengths.data_ptr(), handle), "df11_cache_compact")
-    return cut, numbers[1]
+    if slots < 1:
+        raise ValueError("the new cache needs a slot")
+    p = _flat("pos", pos, torch.int32, device, (B,))
+    k = torch.empty((B, H, slots, D), dtype=dtype, device=device)
+    kept = torch.empty((B, H, slots), dtype=torch.int32, device=device)
+    cut = BoundedCache(k, torch.empty_like(k), torch.empty((B, H, slots), dtype=torch.float32, device=device),
+                       torch.empty_like(kept), torch.empty_like(cache.lengths))
+    rc = lib().df11_cache_compact(cache.args, p, budget, recent, cut.args, kept.data_ptr(), cut.lengths.data_ptr(),
+                                  _stream(device.index))
+    if rc:
+        check(rc, "df11_cache_compact")
+    return cut, kept
 
 
 def verify_drafts(draft_tokens, target_probs, uniforms, draft_probs=None, *, counts=None, stream=None):
@@ -266,27 +290,34 @@ def verify_drafts(draft_tokens, target_probs, uniforms, draft_probs=None, *, cou
     bfloat16 or float16.  Returns tokens [B, G + 1] (the drafts taken, the
     token drawn from max(p - q, 0) or behind the last draft from p, then -1)
     and the number of drafts taken [B] int32."""
-    code = _operand("target_probs", target_probs, _PROBS)
-    _refuse(draft_tokens.dim() != 2 or target_probs.dim() != 3, "draft_tokens must be [B, G], target_probs [B, G + 1, V]")
+    device, dtype = target_probs.device, target_probs.dtype
+    if not _here(device, stream):
+        with _there(device, stream):
+            return verify_drafts(draft_tokens, target_probs, uniforms, draft_probs, counts=counts)
+    code = _code("target_probs", target_probs, _PROBS)
+    if draft_tokens.dim() != 2 or target_probs.dim() != 3:
+        raise ValueError("draft_tokens must be [B, G], target_probs [B, G + 1, V]")
     B, G = draft_tokens.shape
     V = target_probs.shape[2]
-    device = target_probs.device
-    if draft_tokens.dtype not in (torch.int32, torch.int64):
-        raise TypeError("draft_tokens must be int32 or int64, got %s" % draft_tokens.dtype)
-    d = _on("draft_tokens", draft_tokens, draft_tokens.dtype, device)
-    sp = _rows("target_probs", target_probs, target_probs, (B, G + 1, V))
-    sq, q = (0, 0), 0
-    if draft_probs is not None:
-        sq, q = _rows("draft_probs", draft_probs, target_probs, (B, G, V)), draft_probs.data_ptr()
-    u = _on("uniforms", uniforms, torch.float32, device, (B, G + 1))
-    n = _on("counts", counts, torch.int32, device, (B,)) if counts is not None else 0
-    with _Work(device, stream) as handle:
-        tokens = torch.empty((B, G + 1), dtype=draft_tokens.dtype, device=device)
-        accepted = torch.empty((B,), dtype=torch.int32, device=device)
-        args = _VERIFY_ARGS.pack(d, n, target_probs.data_ptr(), q, u, tokens.data_ptr(), accepted.data_ptr(), code,
-                                 draft_tokens.element_size(), B, G, V, sp[0], sp[1], sq[0], sq[1])
-        L = lib()
-        nbytes = L.df11_verify_drafts_workspace_bytes(args)
-        ws = _workspace(nbytes, device) if nbytes else None
-        check(L.df11_verify_drafts(args, ws.data_ptr() if nbytes else 0, nbytes, handle), "df11_verify_drafts")
+    kind = draft_tokens.dtype
+    if kind != torch.int32 and kind != torch.int64:
+        raise TypeError("draft_tokens must be int32 or int64, got %s" % kind)
+    d = _flat("draft_tokens", draft_tokens, kind, device, (B, G))
+    sp = _rows("target_probs", target_probs, dtype, device, (B, G + 1, V))
+    if draft_probs is None:
+        sq, q = (0, 0), 0
+    else:
+        sq, q = _rows("draft_probs", draft_probs, dtype, device, (B, G, V)), draft_probs.data_ptr()
+    u = _flat("uniforms", uniforms, torch.float32, device, (B, G + 1))
+    n = 0 if counts is None else _flat("counts", counts, torch.int32, device, (B,))
+    tokens = torch.empty((B, G + 1), dtype=kind, device=device)
+    accepted = torch.empty((B,), dtype=torch.int32, device=device)
+    args = _VERIFY_ARGS.pack(d, n, target_probs.data_ptr(), q, u, tokens.data_ptr(), accepted.data_ptr(), code,
+                             kind.itemsize, B, G, V, sp[0], sp[1], sq[0], sq[1])
+    L = lib()
+    nbytes = L.df11_verify_drafts_workspace_bytes(args)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    rc = L.df11_verify_drafts(args, ws.data_ptr() if nbytes else 0, nbytes, _stream(device.index))
+    if rc:
+        check(rc, "df11_verify_drafts")
     return tokens, accepted

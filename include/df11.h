@@ -583,7 +583,7 @@ typedef struct df11_verify_args {
 } df11_verify_args;
 
 uint64_t df11_verify_drafts_workspace_bytes(const df11_verify_args *a);
-/* A drafted token outside [0, vocab) is refused (p = q = 0 there).  vocab at
+/* A drafted token outside [0, vocab) is refused (p = q = 0 there).  batch at most 65535, vocab at
  * most 2^22, drafts at most 1024.  Workspace as df11_prefix_attention.  Errors: E_ARG, E_DEVICE. */
 int df11_verify_drafts(const df11_verify_args *a, void *workspace, uint64_t workspace_bytes, void *stream);
 
