@@ -35,6 +35,10 @@ constexpr int kWaves = 4;      // waves of a workgroup, each on every fourth run
 constexpr int kRows = 16;      // rows of a tile
 constexpr int kStep = 32;      // keys of a step
 
+// What a launch's workgroups do: a prefix in 16-row tiles, or in 128-row
+// tiles (both with the sequences' own positions), or bounded caches.
+enum { kRowTiles, kTiles, kCache };
+
 struct Args {
     const uint16_t *q, *prefix_k, *prefix_v, *k, *v;
     const int32_t *lengths, *table, *pos, *positions;
@@ -49,6 +53,7 @@ struct Args {
     float scale2;              // scale * log2(e)
     int32_t prefix_splits, prefix_span, prefix_tiles, suffix_splits, suffix_span, suffix_tiles;
     int64_t rows;              // batch * tokens * heads
+    bool big;                  // the prefix in 128-row tiles
 };
 
 // The 32 keys from `base` on: rows in memory, and which of them which query
@@ -267,21 +272,203 @@ __device__ __forceinline__ void attend_wave(const Src &src, const u32x4 (&q)[DP 
     }
 }
 
+// A tile of 128 rows over a range of keys, by a workgroup: each wave has 32
+// rows, all share the keys and values in LDS, kKeys of them at a time while
+// the next ones are on their way from memory.
+//   S^T = K Q^T    v_mfma_f32_32x32x16: the A operand of lane l is key l % 32,
+//                  dims 16 i + 8 (l / 32) .. + 7 of step i, the B operand the
+//                  same dims of row l % 32.
+//   O^T = V^T P^T  lane l's logits belong to row l % 32 and the keys
+//                  8 (r / 4) + 4 (l / 32) + r % 4: eight of them are the B
+//                  operand of a step of 16 keys, so V is laid out in LDS with
+//                  those eight keys of a dim side by side (turned in registers
+//                  on its way there).
+// LDS: K rows of DP dims and V^T rows of kKeys keys, in 16-byte chunks whose
+// place in the row is exchanged by row so that neighbouring rows lie in
+// different banks (k_at, v_at).
+constexpr int kTileRows = 32 * kWaves;
+
+template <int DP>
+struct TileShape {
+    static constexpr int kKeys = 8192 / DP;          // keys of a step: 16 KB of K and of V
+    static constexpr int kChunks = DP / 8;           // 16-byte chunks of a K row
+    static constexpr int kKeyChunks = kKeys / 8;     // of a V^T row
+    static constexpr int kBuffer = 2 * kKeys * DP * 2;
+    static __device__ __forceinline__ int k_at(int key, int chunk)
+    {
+        const int x = DP == 64 ? (key >> 1) & 7 : key & 15;
+        return key * DP * 2 + (chunk ^ x) * 16;
+    }
+    static __device__ __forceinline__ int v_at(int d, int chunk)
+    {
+        const int x = DP == 64 ? (d ^ (d >> 4)) & 15 : DP == 128 ? ((d >> 1) ^ (d >> 4)) & 7 : ((d >> 2) ^ (d >> 4)) & 3;
+        return kKeys * DP * 2 + d * kKeys * 2 + (chunk ^ x) * 16;
+    }
+};
+
+template <class E, int DP>
+__device__ __forceinline__ void tile_block(const Args &a, char *lds, int head, int tile, int split)
+{
+    typedef TileShape<DP> S;
+    constexpr int kKeys = S::kKeys;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31, g = lane >> 5;
+    const int row_count = a.batch * a.tokens * a.group;
+    const int n = a.prefix, key0 = split * a.prefix_span, key1 = min(n, key0 + a.prefix_span);
+    const uint16_t *kp = a.prefix_k + head * a.prefix_head, *vp = a.prefix_v + head * a.prefix_head;
+
+    const int row = tile * kTileRows + wave * 32 + c;
+    const int t = row / a.group % a.tokens, b = row / (a.group * a.tokens), h = head * a.group + row % a.group;
+    u32x4 q[DP / 16];
+#pragma unroll
+    for (int i = 0; i < DP / 16; i++) {
+        const int d = 16 * i + 8 * g;
+        q[i] = row < row_count && d < a.dim
+                   ? *(const u32x4 *)(a.q + b * a.q_batch + t * a.q_token + h * a.q_head + d)
+                   : u32x4{0, 0, 0, 0};
+    }
+    // what a thread brings: four chunks of K, and four keys by 8 dims of V
+    u32x4 kx[4], vx[4];
+    const int v_quad = threadIdx.x / S::kChunks, v_chunk = threadIdx.x % S::kChunks;
+    const auto load = [&](int base) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int i = threadIdx.x + 256 * j, key = base + i / S::kChunks, d = i % S::kChunks * 8;
+            const u32x4 x = *(const u32x4 *)(kp + (int64_t)min(key, n - 1) * a.prefix_token + (d < a.dim ? d : 0));
+            kx[j] = key < key1 && d < a.dim ? x : u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int key = base + 4 * v_quad + j, d = v_chunk * 8;
+            const u32x4 x = *(const u32x4 *)(vp + (int64_t)min(key, n - 1) * a.prefix_token + (d < a.dim ? d : 0));
+            vx[j] = key < key1 ? x : u32x4{0, 0, 0, 0};
+        }
+    };
+    const auto store = [&](char *to) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int i = threadIdx.x + 256 * j;
+            *(u32x4 *)(to + S::k_at(i / S::kChunks, i % S::kChunks)) = kx[j];
+        }
+        // keys 4 w .. 4 w + 3 of a group of 16: half w / 2 of the chunk of lanes l / 32 = w % 2
+        const int chunk = v_quad / 4 * 2 + (v_quad & 1), half = v_quad >> 1 & 1;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const uint32_t sel = i & 1 ? 0x07060302u : 0x05040100u;
+            const u32x2 x{__builtin_amdgcn_perm(vx[1][i / 2], vx[0][i / 2], sel),
+                          __builtin_amdgcn_perm(vx[3][i / 2], vx[2][i / 2], sel)};
+            *(u32x2 *)(to + S::v_at(v_chunk * 8 + i, chunk) + half * 8) = x;
+        }
+    };
+
+    f32x16 o[DP / 32];
+#pragma unroll
+    for (int i = 0; i < DP / 32; i++)
+#pragma unroll
+        for (int r = 0; r < 16; r++) o[i][r] = 0.0f;
+    float m = -INFINITY, l = 0.0f;
+    load(key0);
+    store(lds);
+    __syncthreads();
+    int buffer = 0;
+    for (int base = key0; base < key1; base += kKeys) {
+        const bool more = base + kKeys < key1;
+        if (more) load(base + kKeys);
+        const char *from = lds + buffer * S::kBuffer;
+        f32x16 s[kKeys / 32];
+#pragma unroll
+        for (int k = 0; k < kKeys / 32; k++) {
+#pragma unroll
+            for (int r = 0; r < 16; r++) s[k][r] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < DP / 16; i++)
+                s[k] = E::mfma32(*(const u32x4 *)(from + S::k_at(32 * k + c, 2 * i + g)), q[i], s[k]);
+        }
+        if (base + kKeys > key1) {
+#pragma unroll
+            for (int k = 0; k < kKeys / 32; k++)
+#pragma unroll
+                for (int r = 0; r < 16; r++)
+                    if (base + 32 * k + 8 * (r / 4) + 4 * g + r % 4 >= key1) s[k][r] = -INFINITY;
+        }
+        float mx = s[0][0];
+#pragma unroll
+        for (int k = 0; k < kKeys / 32; k++)
+#pragma unroll
+            for (int r = 0; r < 16; r++) mx = fmaxf(mx, s[k][r]);
+        mx = fmaxf(mx, __shfl_xor(mx, 32)) * a.scale2;
+        // The running maximum is raised only past 2^8 times itself: a
+        // probability of up to 2^8 is no less exact, and the sums are seldom scaled.
+        const bool raise = mx > m + 8.0f;
+        if (__any(raise)) {
+            const float f = raise ? exp2_fast(m - mx) : 1.0f;
+            m = raise ? mx : m;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < DP / 32; i++) o[i] *= f;
+        }
+        const float safe = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int k = 0; k < kKeys / 32; k++)
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+                u32x4 pb;
+#pragma unroll
+                for (int w = 0; w < 4; w++) {
+                    const float x = exp2_fast(__builtin_fmaf(s[k][8 * half + 2 * w], a.scale2, -safe));
+                    const float y = exp2_fast(__builtin_fmaf(s[k][8 * half + 2 * w + 1], a.scale2, -safe));
+                    l += x + y;
+                    pb[w] = E::pack(x, y);
+                }
+#pragma unroll
+                for (int i = 0; i < DP / 32; i++)
+                    o[i] = E::mfma32(*(const u32x4 *)(from + S::v_at(32 * i + c, 2 * (2 * k + half) + g)), pb, o[i]);
+            }
+        buffer ^= 1;
+        if (more) store(lds + buffer * S::kBuffer);
+        __syncthreads();
+    }
+    l += __shfl_xor(l, 32);
+    if (row < row_count) {
+        const int64_t out_row = ((int64_t)b * a.tokens + t) * a.heads + h;
+        float *to = a.part_o + (split * a.rows + out_row) * a.dim;
+#pragma unroll
+        for (int i = 0; i < DP / 32; i++)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+                const int d = 32 * i + 2 * r + 4 * g;
+                if (d < a.dim) *(f32x4 *)(to + d) = f32x4{o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]};
+            }
+        if (g == 0) a.part_ml[split * a.rows + out_row] = make_float2(m, l);
+    }
+}
+
 // One workgroup: a tile of 16 rows over one range of keys.  Workgroups below
 // the prefix count take a tile of all sequences' rows of one key head over a
 // range of the prefix, the others a tile of one sequence's rows of one key
 // head over a range of its own positions (or of its cache).
-template <class E, int DP, bool CACHE>
-__global__ void __launch_bounds__(64 * kWaves) attend_kernel(const Args a)
+template <class E, int DP, int KIND>
+__global__ void __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) attend_kernel(const Args a)
 {
+    constexpr bool CACHE = KIND == kCache;
     constexpr int W = DP / 16;
-    __shared__ float join_o[kWaves][kRows][DP + 4];
-    __shared__ float2 join_ml[kWaves][kRows];
+    typedef float JoinO[kRows][DP + 4];
+    typedef float2 JoinMl[kRows];
+    constexpr int kJoin = kWaves * (sizeof(JoinO) + sizeof(JoinMl));
+    __shared__ alignas(16) char lds[KIND == kTiles && 2 * TileShape<DP>::kBuffer > kJoin ? 2 * TileShape<DP>::kBuffer : kJoin];
+    JoinO *const join_o = (JoinO *)lds;
+    JoinMl *const join_ml = (JoinMl *)(lds + kWaves * sizeof(JoinO));
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
     const int prefix_items = a.kv_heads * a.prefix_tiles * a.prefix_splits;
-    int item = blockIdx.x;
+    int item = blockIdx.x, split;
     const bool in_prefix = !CACHE && item < prefix_items;
-    int split, tile, head, b = 0;
+    if constexpr (KIND == kTiles) {
+        if (in_prefix) {
+            split = item % a.prefix_splits, item /= a.prefix_splits;
+            tile_block<E, DP>(a, lds, item / a.prefix_tiles, item % a.prefix_tiles, split);
+            return;
+        }
+    }
+    int tile, head, b = 0;
     if (in_prefix) {
         split = item % a.prefix_splits, item /= a.prefix_splits;
         tile = item % a.prefix_tiles, head = item / a.prefix_tiles;
@@ -443,9 +630,11 @@ void plan(Args &a)
 {
     const int64_t want = 8 * df11::cu_count();
     a.rows = (int64_t)a.batch * a.tokens * a.heads;
-    a.prefix_tiles = ceil_div((int64_t)a.batch * a.tokens * a.group, kRows);
+    const int64_t shared_rows = (int64_t)a.batch * a.tokens * a.group;
+    a.big = shared_rows > 32;
+    a.prefix_tiles = ceil_div(shared_rows, a.big ? kTileRows : kRows);
     a.suffix_tiles = ceil_div((int64_t)a.tokens * a.group, kRows);
-    plan_splits(a.prefix, (int64_t)a.prefix_tiles * a.kv_heads, want, &a.prefix_splits, &a.prefix_span);
+    plan_splits(a.prefix, (int64_t)a.prefix_tiles * a.kv_heads, a.big ? 2 * df11::cu_count() : want, &a.prefix_splits, &a.prefix_span);
     plan_splits(a.suffix, (int64_t)a.suffix_tiles * a.kv_heads * a.batch, want, &a.suffix_splits, &a.suffix_span);
 }
 
@@ -481,17 +670,18 @@ int strides_ok(const char *who, std::initializer_list<int64_t> strides)
     return DF11_OK;
 }
 
-template <class E, bool CACHE>
+template <class E, int KIND>
 int launch(const Args &a, hipStream_t st)
 {
+    constexpr bool CACHE = KIND == kCache;
     const int64_t items = (CACHE ? 0 : (int64_t)a.kv_heads * a.prefix_tiles * a.prefix_splits) +
                           (int64_t)a.batch * a.kv_heads * a.suffix_tiles * a.suffix_splits;
     if (items > 0x7fffffffll) return df11::fail(DF11_E_ARG, "attention: too many rows and keys for one launch");
     const dim3 grid((uint32_t)items), block(64 * kWaves);
     if (items) {
-        if (a.dim <= 64) hipLaunchKernelGGL((attend_kernel<E, 64, CACHE>), grid, block, 0, st, a);
-        else if (a.dim <= 128) hipLaunchKernelGGL((attend_kernel<E, 128, CACHE>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((attend_kernel<E, 256, CACHE>), grid, block, 0, st, a);
+        if (a.dim <= 64) hipLaunchKernelGGL((attend_kernel<E, 64, KIND>), grid, block, 0, st, a);
+        else if (a.dim <= 128) hipLaunchKernelGGL((attend_kernel<E, 128, KIND>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((attend_kernel<E, 256, KIND>), grid, block, 0, st, a);
     }
     hipLaunchKernelGGL((join_kernel<E>), dim3((uint32_t)((a.rows + 3) / 4)), dim3(256), 0, st, a);
     if (CACHE && a.suffix)
@@ -543,6 +733,7 @@ int make_prefix(const df11_prefix_attention_args *p, Args &a)
     a.prefix_token = p->prefix_token, a.prefix_head = p->prefix_head;
     a.k_batch = p->k_batch, a.k_token = p->k_token, a.k_head = p->k_head, a.table_batch = p->table_batch;
     a.scale2 = (float)(p->scale * 1.44269504088896340736);
+    if (!(a.scale2 > 0.0f && a.scale2 < INFINITY)) return df11::fail(DF11_E_ARG, "%s: scale must be positive", who);
     plan(a);
     return DF11_OK;
 }
@@ -566,6 +757,7 @@ int make_cache(const df11_cache *c, const df11_cache_attention_args *p, Args &a)
     a.q_batch = p->q_batch, a.q_token = p->q_token, a.q_head = p->q_head;
     a.k_batch = c->stride_batch, a.k_token = c->stride_slot, a.k_head = c->stride_head;
     a.scale2 = (float)(p->scale * 1.44269504088896340736);
+    if (!(a.scale2 > 0.0f && a.scale2 < INFINITY)) return df11::fail(DF11_E_ARG, "%s: scale must be positive", who);
     plan(a);
     a.logit_stride = (c->slots + 31) / 32 * 32;
     return DF11_OK;
@@ -598,8 +790,9 @@ extern "C" int df11_prefix_attention(const df11_prefix_attention_args *p, void *
     rc = check_workspace(who, workspace, workspace_bytes, part_bytes(a));
     if (rc) return rc;
     place(a, workspace);
-    return p->dtype == DF11_FP16 ? launch<Fp16, false>(a, (hipStream_t)stream)
-                                 : launch<Bf16, false>(a, (hipStream_t)stream);
+    hipStream_t st = (hipStream_t)stream;
+    if (a.big) return p->dtype == DF11_FP16 ? launch<Fp16, kTiles>(a, st) : launch<Bf16, kTiles>(a, st);
+    return p->dtype == DF11_FP16 ? launch<Fp16, kRowTiles>(a, st) : launch<Bf16, kRowTiles>(a, st);
 }
 
 extern "C" uint64_t df11_cache_attention_workspace_bytes(const df11_cache *c, const df11_cache_attention_args *p)
@@ -622,5 +815,6 @@ extern "C" int df11_cache_attention(const df11_cache *c, const df11_cache_attent
     rc = check_workspace(who, workspace, workspace_bytes, cache_bytes(a));
     if (rc) return rc;
     place(a, workspace);
-    return c->dtype == DF11_FP16 ? launch<Fp16, true>(a, (hipStream_t)stream) : launch<Bf16, true>(a, (hipStream_t)stream);
+    return c->dtype == DF11_FP16 ? launch<Fp16, kCache>(a, (hipStream_t)stream)
+                                 : launch<Bf16, kCache>(a, (hipStream_t)stream);
 }

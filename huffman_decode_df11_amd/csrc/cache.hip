@@ -80,9 +80,8 @@ constexpr int kSelectWaves = kSelectThreads / 64;
 // then its weight's order, the recent window above all.
 __device__ __forceinline__ uint32_t worth(int32_t at, float w, int32_t pos, int64_t recent)
 {
-    if (at >= pos || at < 0) return 0;
-    if ((int64_t)at >= (int64_t)pos - recent) return 0xffffffffu;
-    return max(1u, order_of(w));
+    const uint32_t late = (int64_t)at >= (int64_t)pos - recent ? 0xffffffffu : 0;
+    return at >= pos || at < 0 ? 0 : max(late, max(1u, order_of(w)));
 }
 
 // One workgroup for each sequence and key head.  A wave holds the worths of

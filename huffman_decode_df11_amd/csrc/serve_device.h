@@ -30,6 +30,11 @@ struct Bf16 {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
                                                        c, 0, 0, 0);
     }
+    static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                       c, 0, 0, 0);
+    }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi)
     {
         return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});
@@ -43,6 +48,11 @@ struct Fp16 {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
                                                       0, 0, 0);
     }
+    static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
+                                                      0, 0, 0);
+    }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi)
     {
         return __builtin_bit_cast(uint32_t, f16x2{(_Float16)lo, (_Float16)hi});
@@ -53,9 +63,9 @@ struct Fp16 {
 // (at most 0xff800000); -0 and +0 are equal.
 __device__ __forceinline__ uint32_t order_of(float w)
 {
-    if (w != w) return 0;
     const uint32_t u = __builtin_bit_cast(uint32_t, w + 0.0f);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    const uint32_t flip = (uint32_t)((int32_t)u >> 31) | 0x80000000u;   // all bits of a negative number, else the sign
+    return w != w ? 0 : u ^ flip;
 }
 
 // The operands of a call, checked: E_ARG texts shared by the entry points.

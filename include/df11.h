@@ -495,7 +495,7 @@ uint64_t df11_prefix_attention_workspace_bytes(const df11_prefix_attention_args 
  * The result does not depend on the run.  Errors: E_ARG (null or misaligned
  * pointer -- 16 bytes for q, k, v and out, strides multiples of 8 -- sizes out of
  * range, dim not a multiple of 8 or above DF11_MAX_DIM, heads not a
- * multiple of kv_heads, workspace too small), E_DEVICE. */
+ * multiple of kv_heads, scale not positive, workspace too small), E_DEVICE. */
 int df11_prefix_attention(const df11_prefix_attention_args *a, void *workspace, uint64_t workspace_bytes,
                           void *stream);
 
