@@ -62,49 +62,71 @@ struct Args {
 struct Keys {
     uint32_t any, all;   // keys that some / every query token sees
     int32_t rel;
-    int64_t row;         // element offset of lane l % 32's key
+    int64_t half[2];     // element offset of the first key of each half, if the halves' rows are evenly spaced
+    int64_t row;         // of lane l % 32's key, if they are not
+};
+
+// What has to come from memory before the keys of a step are known: a
+// source's fetch() starts it two steps ahead, its keys() uses it.
+struct Ahead {
+    int32_t x, y;
 };
 
 struct PrefixSource {
     const uint16_t *k, *v;
     int64_t token;
     int32_t n;
-    __device__ __forceinline__ Keys keys(int base, int lane) const
+    static constexpr bool kEven = true;
+    __device__ __forceinline__ Ahead fetch(int, int) const { return Ahead{0, 0}; }
+    __device__ __forceinline__ Keys keys(Ahead, int base, int) const
     {
         const int left = n - base;
         const uint32_t m = left >= 32 ? 0xffffffffu : (1u << left) - 1;
-        return Keys{m, m, 0, 0};
-    }
-    __device__ __forceinline__ int64_t at(const Keys &, int base, int i) const
-    {
-        return (int64_t)min(base + i, n - 1) * token;
+        return Keys{m, m, 0, {base * token, (base + 16) * token}, 0};
     }
     __device__ __forceinline__ void logits(int, int, int, f32x4) const {}
 };
 
+// EVEN: rows in place, or pages of a multiple of 16 positions.
+template <bool EVEN>
 struct SuffixSource {
     const uint16_t *k, *v;
     const int32_t *table;
     int64_t batch, token;
     int32_t n, tokens, page, n_pages;
-    __device__ __forceinline__ Keys keys(int base, int lane) const
+    static constexpr bool kEven = EVEN;
+    __device__ __forceinline__ Ahead fetch(int base, int lane) const
+    {
+        if (EVEN) {
+            if (!table) return Ahead{0, 0};
+            const int last = (n - 1) / page;
+            return Ahead{table[min(base / page, last)], table[min((base + 16) / page, last)]};
+        }
+        return Ahead{table[min(base + (lane & 31), n - 1) / page], 0};
+    }
+    __device__ __forceinline__ Keys keys(Ahead id, int base, int lane) const
     {
         const int key = base + (lane & 31);
         const int32_t rel = key - (n - tokens);
         bool there = key < n;
-        int64_t row = (int64_t)min(key, n - 1) * token;
-        if (table) {
-            const int p = min(key, n - 1) / page;
-            int32_t id = table[p];
-            there = there && id >= 0 && id < n_pages;
-            id = there ? id : 0;
-            row = (int64_t)id * batch + (int64_t)(min(key, n - 1) - p * page) * token;
+        Keys m;
+        m.row = 0;
+        if (EVEN) {
+            m.half[0] = base * token, m.half[1] = (base + 16) * token;
+            if (table) {
+                const bool in0 = id.x >= 0 && id.x < n_pages, in1 = id.y >= 0 && id.y < n_pages;
+                there = there && (lane & 16 ? in1 : in0);
+                m.half[0] = (in0 ? id.x : 0) * batch + (base % page) * token;
+                m.half[1] = (in1 ? id.y : 0) * batch + ((base + 16) % page) * token;
+            }
+        } else {
+            there = there && id.x >= 0 && id.x < n_pages;
+            m.half[0] = m.half[1] = 0;
+            m.row = (there ? id.x : 0) * batch + (min(key, n - 1) % page) * token;
         }
-        return Keys{(uint32_t)__ballot(there), (uint32_t)__ballot(there && rel <= 0), rel, row};
-    }
-    __device__ __forceinline__ int64_t at(const Keys &m, int base, int i) const
-    {
-        return table ? __shfl(m.row, i) : (int64_t)min(base + i, n - 1) * token;
+        m.any = (uint32_t)__ballot(there), m.all = (uint32_t)__ballot(there && rel <= 0);
+        m.rel = rel;
+        return m;
     }
     __device__ __forceinline__ void logits(int, int, int, f32x4) const {}
 };
@@ -115,18 +137,17 @@ struct CacheSource {
     float *out;          // this row tile's logits
     int64_t token, stride;
     int32_t n, tokens, pos, row_count;
-    __device__ __forceinline__ Keys keys(int base, int lane) const
+    static constexpr bool kEven = true;
+    __device__ __forceinline__ Ahead fetch(int base, int lane) const
     {
-        const int key = base + (lane & 31);
-        const bool in = key < n;
-        const int32_t p = in ? positions[key] : -1;
-        const bool some = p >= 0 && (int64_t)p <= (int64_t)pos + tokens - 1;
-        const int32_t rel = some ? p - pos : 0x7fffffff;
-        return Keys{(uint32_t)__ballot(some), (uint32_t)__ballot(some && rel <= 0), rel, 0};
+        return Ahead{positions[min(base + (lane & 31), n - 1)], 0};
     }
-    __device__ __forceinline__ int64_t at(const Keys &, int base, int i) const
+    __device__ __forceinline__ Keys keys(Ahead at, int base, int lane) const
     {
-        return (int64_t)min(base + i, n - 1) * token;
+        const bool some = base + (lane & 31) < n && at.x >= 0 && (int64_t)at.x <= (int64_t)pos + tokens - 1;
+        const int32_t rel = some ? at.x - pos : 0x7fffffff;
+        return Keys{(uint32_t)__ballot(some), (uint32_t)__ballot(some && rel <= 0), rel,
+                    {base * token, (base + 16) * token}, 0};
     }
     // the logits of row `row`, keys key .. key + 3
     __device__ __forceinline__ void logits(int base, int row, int key, f32x4 s) const
@@ -138,7 +159,9 @@ struct CacheSource {
 // One wave over the keys [key0, key1) of `src`, every `step`-th run of 32.
 // q: this lane's row as B operands; t: its query token.  o[j][r] is, for row
 // lane % 16, dim (4 (lane / 16) + r) * W + j of the sum; m and l its maximum
-// and its sum over this lane's keys.
+// and its sum over this lane's keys.  The next step's keys are on their way
+// while a step's softmax and second product run, its values from behind that
+// product on.
 template <class E, int DP, class Src>
 __device__ __forceinline__ void attend_wave(const Src &src, const u32x4 (&q)[DP / 32], int t, int tokens, int dim,
                                             int key0, int key1, int step, float scale2, f32x4 (&o)[DP / 16], float &m,
@@ -150,44 +173,78 @@ __device__ __forceinline__ void attend_wave(const Src &src, const u32x4 (&q)[DP 
     l = 0.0f;
 #pragma unroll
     for (int j = 0; j < W; j++) o[j] = f32x4{0, 0, 0, 0};
-    for (int base = key0; base < key1; base += step) {
-        const Keys keys = src.keys(base, lane);
-        f32x4 s[2];
-        u32x4 kx[2][DP / 32];
+    if (key0 >= key1) return;
+
+    u32x4 kx[2][DP / 32];
+    uint32_t vx[8][W / 2];
+    // Rows are at a uniform address plus a lane's 32-bit distance: row i of a
+    // half, held back to the last row there is.
+    const auto load_k = [&](const Keys &keys, int base) {
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            const int64_t row = src.at(keys, base, 16 * h + c);
+            const uint16_t *from;
+            if (Src::kEven) {
+                const int most = src.n - 1 - (base + 16 * h);
+                from = src.k + (most < 0 ? keys.half[0] : keys.half[h]) +
+                       (uint32_t)(max(0, min(c, most)) * (int32_t)src.token);
+            } else {
+                from = src.k + __shfl(keys.row, 16 * h + c);
+            }
 #pragma unroll
             for (int i = 0; i < DP / 32; i++) {
                 const int d = 8 * (4 * i + g);
-                kx[h][i] = d < dim ? *(const u32x4 *)(src.k + row + d) : u32x4{0, 0, 0, 0};
+                kx[h][i] = DP == dim || d < dim ? *(const u32x4 *)(from + d) : u32x4{0, 0, 0, 0};
             }
         }
-        uint32_t vx[8][W / 2];
+    };
+    const int vd = min(c * W, dim - (W < 8 ? W : 8));   // a lane past the last dim reads any: its sums go nowhere
+    const auto load_v = [&](const Keys &keys, int base) {
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            const int64_t row = src.at(keys, base, 16 * (j >> 2) + 4 * g + (j & 3));
-            const int d = c * W;
+            const int h = j >> 2, i = 4 * g + (j & 3);
+            const uint16_t *from;
+            if (Src::kEven) {
+                const int most = src.n - 1 - (base + 16 * h);
+                from = src.v + (most < 0 ? keys.half[0] : keys.half[h]) +
+                       (uint32_t)(max(0, min(i, most)) * (int32_t)src.token);
+            } else {
+                from = src.v + __shfl(keys.row, 16 * h + i);
+            }
             if constexpr (W == 4) {
-                const u32x2 x = d < dim ? *(const u32x2 *)(src.v + row + d) : u32x2{0, 0};
+                const u32x2 x = *(const u32x2 *)(from + vd);
                 vx[j][0] = x[0], vx[j][1] = x[1];
             } else {
 #pragma unroll
                 for (int w = 0; w < W / 8; w++) {
-                    const u32x4 x = d + 8 * w < dim ? *(const u32x4 *)(src.v + row + d + 8 * w) : u32x4{0, 0, 0, 0};
+                    const u32x4 x = *(const u32x4 *)(from + min(vd + 8 * w, dim - 8));
 #pragma unroll
                     for (int y = 0; y < 4; y++) vx[j][4 * w + y] = x[y];
                 }
             }
         }
+    };
+
+    Keys keys = src.keys(src.fetch(key0, lane), key0, lane);
+    Ahead ahead = src.fetch(min(key0 + step, key1 - 1) & ~31, lane);
+    load_k(keys, key0);
+    load_v(keys, key0);
+    for (int base = key0; base < key1; base += step) {
+        const int next = base + step;
+        f32x4 s[2];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
             s[h] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < DP / 32; i++) s[h] = E::mfma16(kx[h][i], q[i], s[h]);
         }
+        Keys then = keys;
+        if (next < key1) {
+            then = src.keys(ahead, next, lane);
+            ahead = src.fetch(min(next + step, key1 - 1) & ~31, lane);
+            load_k(then, next);
+        }
         const bool plain = keys.any == keys.all;   // uniform
-        float mx = m;
+        float mx = -INFINITY;
 #pragma unroll
         for (int h = 0; h < 2; h++) {
 #pragma unroll
@@ -205,20 +262,24 @@ __device__ __forceinline__ void attend_wave(const Src &src, const u32x4 (&q)[DP 
         }
         mx = fmaxf(mx, __shfl_xor(mx, 16));
         mx = fmaxf(mx, __shfl_xor(mx, 32));
-        const float safe = mx == -INFINITY ? 0.0f : mx;
-        const float keep = exp2_fast(m - safe);
-        m = mx;
-        l *= keep;
-        float p[8];
+        // The running maximum is raised only past 2^8 times itself: a
+        // probability of up to 2^8 is no less exact, and the sums are seldom scaled.
+        const bool raise = mx > m + 8.0f;
+        if (__any(raise)) {
+            const float f = raise ? exp2_fast(m - mx) : 1.0f;
+            m = raise ? mx : m;
+            l *= f;
 #pragma unroll
-        for (int h = 0; h < 2; h++)
+            for (int j = 0; j < W; j++) o[j] *= f;
+        }
+        const float safe = m == -INFINITY ? 0.0f : m;
+        u32x4 pb;
 #pragma unroll
-            for (int r = 0; r < 4; r++) {
-                p[4 * h + r] = exp2_fast(s[h][r] - safe);
-                l += p[4 * h + r];
-            }
-#pragma unroll
-        for (int j = 0; j < W; j++) o[j] *= keep;
+        for (int w = 0; w < 4; w++) {
+            const float x = exp2_fast(s[w / 2][2 * (w & 1)] - safe), y = exp2_fast(s[w / 2][2 * (w & 1) + 1] - safe);
+            l += x + y;
+            pb[w] = E::pack(x, y);
+        }
         // a key that no row of the tile sees takes part with weight 0: its
         // value must be a number
         if (keys.any != 0xffffffffu) {
@@ -229,46 +290,49 @@ __device__ __forceinline__ void attend_wave(const Src &src, const u32x4 (&q)[DP 
                 for (int w = 0; w < W / 2; w++) vx[j][w] = sees ? vx[j][w] : 0;
             }
         }
-        // The rows of different query tokens see different keys here.  A
+        // The rows of different query tokens may see different keys.  A
         // number times weight 0 is 0; only where a value that some rows must
         // not see is not a number, the tokens take turns, each with its
         // unseen keys cleared and the sums of its own rows kept.
-        int turns = 1;
+        bool odd = false;
         if (!plain) {
-            bool odd = false;
 #pragma unroll
             for (int j = 0; j < 8; j++)
 #pragma unroll
                 for (int w = 0; w < W / 2; w++)
                     odd = odd || (vx[j][w] & E::kExpMask) == E::kExpMask ||
                           ((vx[j][w] >> 16) & E::kExpMask) == E::kExpMask;
-            if (__any(odd)) turns = tokens;
         }
-        int32_t rel[8];
+        if (!plain && __any(odd)) {
+            for (int turn = 0; turn < tokens; turn++) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) rel[j] = plain ? 0 : __shfl(keys.rel, 16 * (j >> 2) + 4 * g + (j & 3));
-        for (int turn = 0; turn < turns; turn++) {
-            const bool mine = turns == 1 || t == turn;
-            u32x4 pb;
+                for (int j = 0; j < W; j++) {
+                    u32x4 va;
 #pragma unroll
-            for (int w = 0; w < 4; w++) pb[w] = E::pack(p[2 * w], p[2 * w + 1]);
+                    for (int w = 0; w < 4; w++) {
+                        const int i = 16 * (w >> 1) + 4 * g + 2 * (w & 1);
+                        const int32_t rel_lo = __shfl(keys.rel, i), rel_hi = __shfl(keys.rel, i + 1);
+                        const uint32_t lo = rel_lo <= turn ? vx[2 * w][j / 2] : 0;
+                        const uint32_t hi = rel_hi <= turn ? vx[2 * w + 1][j / 2] : 0;
+                        va[w] = __builtin_amdgcn_perm(hi, lo, j & 1 ? 0x07060302u : 0x05040100u);
+                    }
+                    const f32x4 sum = E::mfma16(va, pb, o[j]);
+#pragma unroll
+                    for (int r = 0; r < 4; r++) o[j][r] = t == turn ? sum[r] : o[j][r];
+                }
+            }
+        } else {
 #pragma unroll
             for (int j = 0; j < W; j++) {
                 u32x4 va;
 #pragma unroll
-                for (int w = 0; w < 4; w++) {
-                    uint32_t lo = vx[2 * w][j / 2], hi = vx[2 * w + 1][j / 2];
-                    if (turns > 1) {
-                        lo = rel[2 * w] <= turn ? lo : 0;
-                        hi = rel[2 * w + 1] <= turn ? hi : 0;
-                    }
-                    va[w] = __builtin_amdgcn_perm(hi, lo, j & 1 ? 0x07060302u : 0x05040100u);
-                }
-                const f32x4 sum = E::mfma16(va, pb, o[j]);
-#pragma unroll
-                for (int r = 0; r < 4; r++) o[j][r] = mine ? sum[r] : o[j][r];
+                for (int w = 0; w < 4; w++)
+                    va[w] = __builtin_amdgcn_perm(vx[2 * w + 1][j / 2], vx[2 * w][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
+                o[j] = E::mfma16(va, pb, o[j]);
             }
         }
+        if (next < key1) load_v(then, next);
+        keys = then;
     }
 }
 
@@ -512,9 +576,14 @@ __global__ void __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) attend_kernel(
         attend_wave<E, DP>(src, q, t, a.tokens, a.dim, first, key1, kStep * kWaves, a.scale2, o, m, l);
     } else {
         const int64_t at = (a.table ? 0 : b * a.k_batch) + head * a.k_head;
-        const SuffixSource src{a.k + at, a.v + at, a.table ? a.table + b * a.table_batch : nullptr, a.k_batch,
-                               a.k_token, n, a.tokens, a.page, a.n_pages};
-        attend_wave<E, DP>(src, q, t, a.tokens, a.dim, first, key1, kStep * kWaves, a.scale2, o, m, l);
+        const int32_t *table = a.table ? a.table + b * a.table_batch : nullptr;
+        if (!a.table || a.page % 16 == 0) {
+            const SuffixSource<true> src{a.k + at, a.v + at, table, a.k_batch, a.k_token, n, a.tokens, a.page, a.n_pages};
+            attend_wave<E, DP>(src, q, t, a.tokens, a.dim, first, key1, kStep * kWaves, a.scale2, o, m, l);
+        } else {
+            const SuffixSource<false> src{a.k + at, a.v + at, table, a.k_batch, a.k_token, n, a.tokens, a.page, a.n_pages};
+            attend_wave<E, DP>(src, q, t, a.tokens, a.dim, first, key1, kStep * kWaves, a.scale2, o, m, l);
+        }
     }
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
@@ -552,83 +621,129 @@ __device__ __forceinline__ int own_splits(const Args &a, int b)
     return (n + a.suffix_span - 1) / a.suffix_span;
 }
 
-// The joined maximum and sum of an output row.
-__device__ __forceinline__ float2 join_row(const Args &a, int64_t row, int own)
+constexpr int kMostParts = 256;   // ranges of keys that a row's sums are joined from
+
+// One wave: the maximum and the sum of a row's ranges, of which lane l has
+// every 64th.
+__device__ __forceinline__ float2 join_row(const Args &a, int64_t row, int parts)
 {
+    const int lane = threadIdx.x & 63;
     float m = -INFINITY, l = 0.0f;
-    for (int s = 0; s < a.prefix_splits + own; s++) m = fmaxf(m, a.part_ml[s * a.rows + row].x);
-    const float safe = m == -INFINITY ? 0.0f : m;
-    for (int s = 0; s < a.prefix_splits + own; s++) {
+    for (int s = lane; s < parts; s += 64) {
         const float2 x = a.part_ml[s * a.rows + row];
-        l += exp2_fast(x.x - safe) * x.y;
+        const float top = fmaxf(m, x.x), safe = top == -INFINITY ? 0.0f : top;
+        l = exp2_fast(m - safe) * l + exp2_fast(x.x - safe) * x.y;
+        m = top;
+    }
+    for (int d = 32; d; d >>= 1) {
+        const float om = __shfl_xor(m, d), ol = __shfl_xor(l, d);
+        const float top = fmaxf(m, om), safe = top == -INFINITY ? 0.0f : top;
+        const float x = exp2_fast(m - safe) * l, y = exp2_fast(om - safe) * ol;
+        l = x + y;
+        m = top;
     }
     return make_float2(m, l);
 }
 
-// One wave joins the ranges of one output row.
+// One workgroup joins the ranges of one output row: each wave takes every
+// fourth range, each lane two dims.
 template <class E>
-__global__ void __launch_bounds__(256) join_kernel(const Args a)
+__device__ __forceinline__ void join_block(const Args &a, int64_t row)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= a.rows) return;
-    const int b = (int)(row / ((int64_t)a.tokens * a.heads));
-    const int own = own_splits(a, b);
-    const float2 ml = join_row(a, row, own);
+    __shared__ float factor[kMostParts];
+    __shared__ float2 sums[kWaves][DF11_MAX_DIM / 2];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int parts = a.prefix_splits + own_splits(a, (int)(row / ((int64_t)a.tokens * a.heads)));
+    const float2 ml = join_row(a, row, parts);
     const float safe = ml.x == -INFINITY ? 0.0f : ml.x;
-    const float inv = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
+    if (threadIdx.x < parts) factor[threadIdx.x] = exp2_fast(a.part_ml[threadIdx.x * a.rows + row].x - safe);
+    __syncthreads();
     for (int d = 2 * lane; d < a.dim; d += 128) {
         float x = 0.0f, y = 0.0f;
-        for (int s = 0; s < a.prefix_splits + own; s++) {
-            const float f = exp2_fast(a.part_ml[s * a.rows + row].x - safe);
+#pragma unroll 4
+        for (int s = wave; s < parts; s += kWaves) {
             const float2 o = *(const float2 *)(a.part_o + (s * a.rows + row) * a.dim + d);
-            x += f * o.x, y += f * o.y;
+            x += factor[s] * o.x, y += factor[s] * o.y;
         }
-        *(uint32_t *)(a.out + row * a.dim + d) = E::pack(x * inv, y * inv);
+        sums[wave][d / 2] = make_float2(x, y);
     }
-    if (a.lse && lane == 0) a.lse[row] = ml.y == 0.0f ? -INFINITY : kLn2 * (ml.x + __log2f(ml.y));
+    __syncthreads();
+    const float inv = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
+    if (2 * threadIdx.x < a.dim) {
+        float x = 0.0f, y = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; w++) x += sums[w][threadIdx.x].x, y += sums[w][threadIdx.x].y;
+        *(uint32_t *)(a.out + row * a.dim + 2 * threadIdx.x) = E::pack(x * inv, y * inv);
+    }
+    if (a.lse && threadIdx.x == 0) a.lse[row] = ml.y == 0.0f ? -INFINITY : kLn2 * (ml.x + __log2f(ml.y));
 }
 
-// A slot's weight: the probabilities that the rows of its head gave it.
-__global__ void __launch_bounds__(256) weigh_kernel(const Args a)
+constexpr int kWeighKeys = 1024;   // slots of a workgroup, four to a thread
+
+// The weights of a run of a head's slots: the probabilities that the rows of
+// the head gave them.
+__device__ __forceinline__ void weigh_block(const Args &a, int bh, int first)
 {
-    __shared__ float top[256];
-    const int bh = blockIdx.y, b = bh / a.kv_heads, head = bh % a.kv_heads;
+    __shared__ float top[64];
+    const int b = bh / a.kv_heads, head = bh % a.kv_heads;
     const int n = max(0, min(a.lengths[b], a.suffix));
-    const int key = blockIdx.x * 256 + threadIdx.x;
-    if ((int)(blockIdx.x * 256) >= n) return;
-    const int row_count = a.tokens * a.group, own = own_splits(a, b);
-    float w = 0.0f;
-    for (int r0 = 0; r0 < row_count; r0 += 256) {
+    if (first >= n) return;
+    const int key = first + 4 * threadIdx.x;
+    const int row_count = a.tokens * a.group, parts = own_splits(a, b), wave = threadIdx.x >> 6;
+    float w[4] = {0, 0, 0, 0};
+    for (int r0 = 0; r0 < row_count; r0 += 64) {
+        const int some = min(64, row_count - r0);
         __syncthreads();
-        const int r = r0 + threadIdx.x;
-        if (r < row_count) {
-            const int64_t row = ((int64_t)b * a.tokens + r / a.group) * a.heads + head * a.group + r % a.group;
-            const float2 ml = join_row(a, row, own);
-            top[threadIdx.x] = ml.y == 0.0f ? INFINITY : ml.x + __log2f(ml.y);   // an empty row gives nothing
+        for (int r = wave; r < some; r += kWaves) {
+            const int t = (r0 + r) / a.group, h = (r0 + r) % a.group;
+            const float2 ml = join_row(a, ((int64_t)b * a.tokens + t) * a.heads + head * a.group + h, parts);
+            if ((threadIdx.x & 63) == 0) top[r] = ml.y == 0.0f ? INFINITY : ml.x + __log2f(ml.y);   // an empty row gives nothing
         }
         __syncthreads();
-        if (key < n)
-            for (int i = 0; i < min(256, row_count - r0); i++)
-                w += exp2_fast(a.logits[((int64_t)bh * row_count + r0 + i) * a.logit_stride + key] - top[i]);
+        if (key < n) {
+            const float *from = a.logits + ((int64_t)bh * row_count + r0) * a.logit_stride + key;
+#pragma unroll 4
+            for (int i = 0; i < some; i++) {
+                const f32x4 s = *(const f32x4 *)(from + i * a.logit_stride);
+#pragma unroll
+                for (int j = 0; j < 4; j++) w[j] += exp2_fast(s[j] - top[i]);
+            }
+        }
     }
-    if (key < n) a.weights[(int64_t)bh * a.suffix + key] += w;
+    float *to = a.weights + (int64_t)bh * a.suffix + key;
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        if (key + j < n) to[j] += w[j];
+}
+
+// Workgroups below the number of output rows join one row each; behind them
+// those of bounded caches add up the slots' weights.
+template <class E, int KIND>
+__global__ void __launch_bounds__(64 * kWaves) finish_kernel(const Args a)
+{
+    if (KIND != kCache || blockIdx.x < a.rows) {
+        join_block<E>(a, blockIdx.x);
+    } else {
+        const int runs = (a.suffix + kWeighKeys - 1) / kWeighKeys, item = blockIdx.x - (int)a.rows;
+        weigh_block(a, item / runs, item % runs * kWeighKeys);
+    }
 }
 
 int ceil_div(int64_t x, int64_t y) { return (int)((x + y - 1) / y); }
 
-// Ranges of at least 256 keys, enough of them for `want` workgroups in all.
+// Ranges of at least a step of every wave, enough of them for `want`
+// workgroups in all.
 void plan_splits(int64_t keys, int64_t items, int64_t want, int32_t *splits, int32_t *span)
 {
-    const int64_t most = std::max<int64_t>(1, keys / 256);
-    const int64_t n = std::max<int64_t>(1, std::min(most, want / std::max<int64_t>(1, items)));
-    *span = ceil_div(ceil_div(std::max<int64_t>(keys, 1), n), kStep * kWaves) * kStep * kWaves;
+    constexpr int64_t kLeast = kStep * kWaves;
+    const int64_t n = std::max<int64_t>(1, std::min<int64_t>(kMostParts / 2, want / std::max<int64_t>(1, items)));
+    *span = ceil_div(ceil_div(std::max<int64_t>(keys, 1), n), kLeast) * kLeast;
     *splits = keys ? ceil_div(keys, *span) : 0;
 }
 
 void plan(Args &a)
 {
-    const int64_t want = 8 * df11::cu_count();
+    const int64_t want = 4 * df11::cu_count();
     a.rows = (int64_t)a.batch * a.tokens * a.heads;
     const int64_t shared_rows = (int64_t)a.batch * a.tokens * a.group;
     a.big = shared_rows > 32;
@@ -663,10 +778,13 @@ int check_heads(const char *who, int64_t dtype, int64_t batch, int64_t tokens, i
     return DF11_OK;
 }
 
-int strides_ok(const char *who, std::initializer_list<int64_t> strides)
+int strides_ok(const char *who, std::initializer_list<int64_t> strides, std::initializer_list<int64_t> rows)
 {
     for (int64_t s : strides)
         if (s < 0 || s % 8) return df11::fail(DF11_E_ARG, "%s: stride %lld is not a multiple of 8", who, (long long)s);
+    // a lane's distance within 16 rows is a 32-bit number
+    for (int64_t s : rows)
+        if (s >= 1ll << 27) return df11::fail(DF11_E_ARG, "%s: rows %lld elements apart", who, (long long)s);
     return DF11_OK;
 }
 
@@ -683,9 +801,9 @@ int launch(const Args &a, hipStream_t st)
         else if (a.dim <= 128) hipLaunchKernelGGL((attend_kernel<E, 128, KIND>), grid, block, 0, st, a);
         else hipLaunchKernelGGL((attend_kernel<E, 256, KIND>), grid, block, 0, st, a);
     }
-    hipLaunchKernelGGL((join_kernel<E>), dim3((uint32_t)((a.rows + 3) / 4)), dim3(256), 0, st, a);
-    if (CACHE && a.suffix)
-        hipLaunchKernelGGL(weigh_kernel, dim3(ceil_div(a.suffix, 256), a.batch * a.kv_heads), dim3(256), 0, st, a);
+    const int64_t finish = a.rows + (CACHE ? (int64_t)a.batch * a.kv_heads * ceil_div(a.suffix, kWeighKeys) : 0);
+    if (finish > 0x7fffffffll) return df11::fail(DF11_E_ARG, "attention: too many rows and slots for one launch");
+    hipLaunchKernelGGL((finish_kernel<E, KIND>), dim3((uint32_t)finish), block, 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return df11::fail(DF11_E_DEVICE, "attention launch: %s", hipGetErrorString(e));
     return DF11_OK;
@@ -717,7 +835,7 @@ int make_prefix(const df11_prefix_attention_args *p, Args &a)
         (p->block_table && (!small(p->page, 1, kMost) || !small(p->n_pages, 0, kMost) || p->suffix % p->page)))
         return df11::fail(DF11_E_ARG, "%s: prefix, suffix or page sizes out of range", who);
     rc = strides_ok(who, {p->q_batch, p->q_token, p->q_head, p->prefix_token, p->prefix_head, p->k_batch, p->k_token,
-                          p->k_head});
+                          p->k_head}, {p->prefix_token, p->k_token});
     if (rc) return rc;
     if (p->table_batch < 0) return df11::fail(DF11_E_ARG, "%s: negative table stride", who);
     a.q = (const uint16_t *)p->q;
@@ -746,7 +864,8 @@ int make_cache(const df11_cache *c, const df11_cache_attention_args *p, Args &a)
     if (rc) return rc;
     if (!small(c->slots, 0, kMost) || (double)c->batch * c->kv_heads > 65535)
         return df11::fail(DF11_E_ARG, "%s: slots or batch * kv_heads out of range", who);
-    rc = strides_ok(who, {p->q_batch, p->q_token, p->q_head, c->stride_batch, c->stride_head, c->stride_slot});
+    rc = strides_ok(who, {p->q_batch, p->q_token, p->q_head, c->stride_batch, c->stride_head, c->stride_slot},
+                    {c->stride_slot});
     if (rc) return rc;
     a.q = (const uint16_t *)p->q;
     a.k = (const uint16_t *)c->k, a.v = (const uint16_t *)c->v;
