@@ -368,6 +368,18 @@ struct TileShape {
         const int x = DP == 64 ? (d ^ (d >> 4)) & 15 : DP == 128 ? ((d >> 1) ^ (d >> 4)) & 7 : ((d >> 2) ^ (d >> 4)) & 3;
         return kKeys * DP * 2 + d * kKeys * 2 + (chunk ^ x) * 16;
     }
+    // The same places by exclusive or with one lane's first one: chunk + 2 i
+    // of a K row (chunk < 2); dim d + i, i < 8, of V^T (d a multiple of 8);
+    // dim d + 32 i and chunk + 2 j of V^T (d < 32, chunk < 2).
+    static __device__ __forceinline__ int k_next(int first, int i) { return first ^ (2 * i * 16); }
+    static __device__ __forceinline__ int v_next_dim(int first, int i)
+    {
+        return (first ^ ((DP == 64 ? i : DP == 128 ? i / 2 : i / 4) * 16)) + i * kKeys * 2;
+    }
+    static __device__ __forceinline__ int v_next(int first, int i, int j)
+    {
+        return (first ^ (((i ^ j) & (kKeyChunks / 2 - 1)) * 32)) + 32 * i * kKeys * 2;
+    }
 };
 
 template <class E, int DP>
@@ -390,37 +402,58 @@ __device__ __forceinline__ void tile_block(const Args &a, char *lds, int head, i
                    ? *(const u32x4 *)(a.q + b * a.q_batch + t * a.q_token + h * a.q_head + d)
                    : u32x4{0, 0, 0, 0};
     }
-    // what a thread brings: four chunks of K, and four keys by 8 dims of V
+    // What a thread brings: four chunks of K, and four keys by 8 dims of V,
+    // at a uniform address plus its own 32-bit distance.
     u32x4 kx[4], vx[4];
     const int v_quad = threadIdx.x / S::kChunks, v_chunk = threadIdx.x % S::kChunks;
+    const int32_t token = (int32_t)a.prefix_token;
+    const int my_d = v_chunk * 8 < a.dim ? v_chunk * 8 : 0;
+    const bool pad = v_chunk * 8 >= a.dim;   // dims that K does not have take part as 0
+    const uint32_t k_far = (uint32_t)(v_quad * token) + my_d, v_far = (uint32_t)(4 * v_quad * token) + my_d;
+    constexpr int kRowsEach = 256 / S::kChunks;   // keys between a thread's chunks of K
     const auto load = [&](int base) {
+        if (base + kKeys <= key1) {
+            const uint16_t *k = kp + base * a.prefix_token, *v = vp + base * a.prefix_token;
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const int i = threadIdx.x + 256 * j, key = base + i / S::kChunks, d = i % S::kChunks * 8;
-            const u32x4 x = *(const u32x4 *)(kp + (int64_t)min(key, n - 1) * a.prefix_token + (d < a.dim ? d : 0));
-            kx[j] = key < key1 && d < a.dim ? x : u32x4{0, 0, 0, 0};
-        }
+            for (int j = 0; j < 4; j++) {
+                kx[j] = *(const u32x4 *)(k + (int64_t)(kRowsEach * j) * a.prefix_token + k_far);
+                vx[j] = *(const u32x4 *)(v + j * a.prefix_token + v_far);
+            }
+        } else {
+            // the last step: keys past the end are 0
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const int key = base + 4 * v_quad + j, d = v_chunk * 8;
-            const u32x4 x = *(const u32x4 *)(vp + (int64_t)min(key, n - 1) * a.prefix_token + (d < a.dim ? d : 0));
-            vx[j] = key < key1 ? x : u32x4{0, 0, 0, 0};
+            for (int j = 0; j < 4; j++) {
+                const int kk = base + kRowsEach * j + v_quad, kv = base + 4 * v_quad + j;
+                const u32x4 x = *(const u32x4 *)(kp + min(kk, n - 1) * a.prefix_token + my_d);
+                const u32x4 y = *(const u32x4 *)(vp + min(kv, n - 1) * a.prefix_token + my_d);
+#pragma unroll
+                for (int w = 0; w < 4; w++) kx[j][w] = kk < key1 ? x[w] : 0, vx[j][w] = kv < key1 ? y[w] : 0;
+            }
         }
     };
-    const auto store = [&](char *to) {
+    const int k_to = S::k_at(v_quad, v_chunk);
+    // keys 4 w .. 4 w + 3 of a group of 16: half w / 2 of the chunk of lanes l / 32 = w % 2
+    const int v_to = S::v_at(v_chunk * 8, v_quad / 4 * 2 + (v_quad & 1)) + (v_quad >> 1 & 1) * 8;
+    const auto store = [&](int buffer) {
+        if (a.dim < DP) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+#pragma unroll
+                for (int w = 0; w < 4; w++) kx[j][w] = pad ? 0 : kx[j][w];
+        }
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            const int i = threadIdx.x + 256 * j;
-            *(u32x4 *)(to + S::k_at(i / S::kChunks, i % S::kChunks)) = kx[j];
+            // rows a multiple of 16 apart exchange their chunks alike
+            if (DP < 256) *(u32x4 *)(lds + k_to + buffer + j * kRowsEach * DP * 2) = kx[j];
+            else *(u32x4 *)(lds + buffer + S::k_at(v_quad + kRowsEach * j, v_chunk)) = kx[j];
         }
-        // keys 4 w .. 4 w + 3 of a group of 16: half w / 2 of the chunk of lanes l / 32 = w % 2
-        const int chunk = v_quad / 4 * 2 + (v_quad & 1), half = v_quad >> 1 & 1;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             const uint32_t sel = i & 1 ? 0x07060302u : 0x05040100u;
             const u32x2 x{__builtin_amdgcn_perm(vx[1][i / 2], vx[0][i / 2], sel),
                           __builtin_amdgcn_perm(vx[3][i / 2], vx[2][i / 2], sel)};
-            *(u32x2 *)(to + S::v_at(v_chunk * 8 + i, chunk) + half * 8) = x;
+            *(u32x2 *)(lds + buffer + S::v_next_dim(v_to, i)) = x;
         }
     };
 
@@ -430,33 +463,51 @@ __device__ __forceinline__ void tile_block(const Args &a, char *lds, int head, i
 #pragma unroll
         for (int r = 0; r < 16; r++) o[i][r] = 0.0f;
     float m = -INFINITY, l = 0.0f;
-    load(key0);
-    store(lds);
-    __syncthreads();
-    int buffer = 0;
-    for (int base = key0; base < key1; base += kKeys) {
-        const bool more = base + kKeys < key1;
-        if (more) load(base + kKeys);
-        const char *from = lds + buffer * S::kBuffer;
-        f32x16 s[kKeys / 32];
+    // A step's operands in the order of its products: the K rows, each 32 keys
+    // in turn, then the V^T rows of each 16 keys; kAhead of them are on their way.
+    constexpr int kK = DP / 16, kParts = kKeys / 32, kV = 2 * (DP / 32), kFrags = kParts * (kK + kV), kAhead = 4;
+    const int k_from = S::k_at(c, g), v_from = S::v_at(c, g);
+    const auto frag = [&](int buffer, int i) {
+        int at;
+        if (i < kParts * kK) {
+            at = S::k_next(k_from, i / kParts) + 32 * (i % kParts) * DP * 2;
+        } else {
+            i -= kParts * kK;
+            at = S::v_next(v_from, i % (DP / 32), i / (DP / 32));
+        }
+        return *(const u32x4 *)(lds + buffer + at);
+    };
+    const auto step = [&](int buffer, int left) {
+        f32x16 s[kParts];
+        u32x4 f[kFrags];
 #pragma unroll
-        for (int k = 0; k < kKeys / 32; k++) {
+        for (int i = 0; i < kAhead; i++) f[i] = frag(buffer, i);
+#pragma unroll
+        for (int k = 0; k < kParts; k++)
 #pragma unroll
             for (int r = 0; r < 16; r++) s[k][r] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < DP / 16; i++)
-                s[k] = E::mfma32(*(const u32x4 *)(from + S::k_at(32 * k + c, 2 * i + g)), q[i], s[k]);
+        for (int i = 0; i < kParts * kK; i++) {
+            f[i + kAhead] = frag(buffer, i + kAhead);
+            s[i % kParts] = E::mfma32(f[i], q[i / kParts], s[i % kParts]);
         }
-        if (base + kKeys > key1) {
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
 #pragma unroll
-            for (int k = 0; k < kKeys / 32; k++)
+        for (int i = 0; i < kParts * kK; i++) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        if (left < kKeys) {
+            __builtin_amdgcn_sched_barrier(0);   // a branch of its own: no step but the last pays for it
+#pragma unroll
+            for (int k = 0; k < kParts; k++)
 #pragma unroll
                 for (int r = 0; r < 16; r++)
-                    if (base + 32 * k + 8 * (r / 4) + 4 * g + r % 4 >= key1) s[k][r] = -INFINITY;
+                    if (32 * k + 8 * (r / 4) + 4 * g + r % 4 >= left) s[k][r] = -INFINITY;
         }
         float mx = s[0][0];
 #pragma unroll
-        for (int k = 0; k < kKeys / 32; k++)
+        for (int k = 0; k < kParts; k++)
 #pragma unroll
             for (int r = 0; r < 16; r++) mx = fmaxf(mx, s[k][r]);
         mx = fmaxf(mx, __shfl_xor(mx, 32)) * a.scale2;
@@ -464,15 +515,15 @@ __device__ __forceinline__ void tile_block(const Args &a, char *lds, int head, i
         // probability of up to 2^8 is no less exact, and the sums are seldom scaled.
         const bool raise = mx > m + 8.0f;
         if (__any(raise)) {
-            const float f = raise ? exp2_fast(m - mx) : 1.0f;
+            const float by = raise ? exp2_fast(m - mx) : 1.0f;
             m = raise ? mx : m;
-            l *= f;
+            l *= by;
 #pragma unroll
-            for (int i = 0; i < DP / 32; i++) o[i] *= f;
+            for (int i = 0; i < DP / 32; i++) o[i] *= by;
         }
         const float safe = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-        for (int k = 0; k < kKeys / 32; k++)
+        for (int k = 0; k < kParts; k++)
 #pragma unroll
             for (int half = 0; half < 2; half++) {
                 u32x4 pb;
@@ -484,12 +535,35 @@ __device__ __forceinline__ void tile_block(const Args &a, char *lds, int head, i
                     pb[w] = E::pack(x, y);
                 }
 #pragma unroll
-                for (int i = 0; i < DP / 32; i++)
-                    o[i] = E::mfma32(*(const u32x4 *)(from + S::v_at(32 * i + c, 2 * (2 * k + half) + g)), pb, o[i]);
+                for (int i = 0; i < DP / 32; i++) {
+                    const int at = kParts * kK + (2 * k + half) * (DP / 32) + i;
+                    if (at + kAhead < kFrags) f[at + kAhead] = frag(buffer, at + kAhead);
+                    o[i] = E::mfma32(f[at], pb, o[i]);
+                }
             }
-        buffer ^= 1;
-        if (more) store(lds + buffer * S::kBuffer);
-        __syncthreads();
+        __builtin_amdgcn_sched_group_barrier(0x402, 8 * 2 + 4, 0);
+#pragma unroll
+        for (int i = 0; i < kFrags - kParts * kK; i++) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            if (i < kFrags - kParts * kK - kAhead) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x402, 7, 0);
+        }
+    };
+
+    load(key0);
+    store(0);
+    __syncthreads();
+    for (int base = key0; base < key1; base += 2 * kKeys) {
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+            const int at = base + half * kKeys;
+            if (at >= key1) break;
+            const bool more = at + kKeys < key1;
+            if (more) load(at + kKeys);
+            step(half * S::kBuffer, key1 - at);
+            if (more) store((1 - half) * S::kBuffer);
+            __syncthreads();
+        }
     }
     l += __shfl_xor(l, 32);
     if (row < row_count) {
@@ -518,7 +592,7 @@ __global__ void __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) attend_kernel(
     typedef float JoinO[kRows][DP + 4];
     typedef float2 JoinMl[kRows];
     constexpr int kJoin = kWaves * (sizeof(JoinO) + sizeof(JoinMl));
-    __shared__ alignas(16) char lds[KIND == kTiles && 2 * TileShape<DP>::kBuffer > kJoin ? 2 * TileShape<DP>::kBuffer : kJoin];
+    __shared__ alignas(1024) char lds[KIND == kTiles && 2 * TileShape<DP>::kBuffer > kJoin ? 2 * TileShape<DP>::kBuffer : kJoin];
     JoinO *const join_o = (JoinO *)lds;
     JoinMl *const join_ml = (JoinMl *)(lds + kWaves * sizeof(JoinO));
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
