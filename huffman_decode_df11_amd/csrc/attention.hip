@@ -23,6 +23,7 @@
 //                8 x W block in registers (v_perm_b32); product j of the W
 //                takes the dims j, W + j, 2 W + j, ...
 #include <algorithm>
+#include <cmath>
 
 #include "df11_internal.h"
 #include "serve_device.h"
@@ -805,26 +806,52 @@ __global__ void __launch_bounds__(64 * kWaves) finish_kernel(const Args a)
 
 int ceil_div(int64_t x, int64_t y) { return (int)((x + y - 1) / y); }
 
-// Ranges of at least a step of every wave, enough of them for `want`
-// workgroups in all.
-void plan_splits(int64_t keys, int64_t items, int64_t want, int32_t *splits, int32_t *span)
+// The keys of an item in n ranges, of at least a step of every wave.
+void set_ranges(int64_t keys, int64_t n, int32_t *splits, int32_t *span)
 {
     constexpr int64_t kLeast = kStep * kWaves;
-    const int64_t n = std::max<int64_t>(1, std::min<int64_t>(kMostParts / 2, want / std::max<int64_t>(1, items)));
+    n = std::max<int64_t>(1, std::min<int64_t>(kMostParts / 2, n));
     *span = ceil_div(ceil_div(std::max<int64_t>(keys, 1), n), kLeast) * kLeast;
     *splits = keys ? ceil_div(keys, *span) : 0;
 }
 
+// The fewest ranges with which all items' workgroups nearly fill the `slots`
+// that are resident at a time, once or several times over: 528 items of 4099
+// keys on 768 slots 120 us in 2 ranges, 102 in 4; 512 items of 2048 keys on
+// 512 slots 100 us in 1 range, 102 in 2.
+int64_t ranges_that_fill(int64_t keys, int64_t items, int64_t slots)
+{
+    const int64_t most = std::min<int64_t>(ceil_div(keys, kStep * kWaves), ceil_div(8 * slots, items));
+    int64_t best = 1;
+    double full = 0.0;
+    for (int64_t n = 1; n <= most && full < 0.9; n++) {
+        const double rounds = (double)items * n / slots, x = rounds / std::ceil(rounds);
+        if (x > full) full = x, best = n;
+    }
+    return best;
+}
+
 void plan(Args &a)
 {
-    const int64_t want = 4 * df11::cu_count();
+    const int64_t cus = df11::cu_count();
+    const int64_t resident = a.dim <= 64 ? 3 : a.dim <= 128 ? 2 : 1;   // workgroups of a CU, by the kernels' registers
     a.rows = (int64_t)a.batch * a.tokens * a.heads;
+    if (!a.rows) return;
     const int64_t shared_rows = (int64_t)a.batch * a.tokens * a.group;
     a.big = shared_rows > 32;
     a.prefix_tiles = ceil_div(shared_rows, a.big ? kTileRows : kRows);
     a.suffix_tiles = ceil_div((int64_t)a.tokens * a.group, kRows);
-    plan_splits(a.prefix, (int64_t)a.prefix_tiles * a.kv_heads, a.big ? 2 * df11::cu_count() : want, &a.prefix_splits, &a.prefix_span);
-    plan_splits(a.suffix, (int64_t)a.suffix_tiles * a.kv_heads * a.batch, want, &a.suffix_splits, &a.suffix_span);
+    // 128-row tiles: one workgroup on each CU, whose partial sums are few and
+    // which leaves room for those of the sequences' own positions; two where
+    // a long prefix is nearly all there is (128 requests behind 32768
+    // positions with 1024 / 1 of their own: 137 / 130 us with one, 157 / 109
+    // with two; 64 requests behind 8191: 29 us with one, 37 with two).
+    const int64_t prefix_items = (int64_t)a.prefix_tiles * a.kv_heads;
+    const bool alone = 4ll * a.batch * a.suffix <= a.prefix && a.prefix * prefix_items >= 2048 * cus;
+    set_ranges(a.prefix, a.big ? (alone ? 2 : 1) * cus / prefix_items : ranges_that_fill(a.prefix, prefix_items, resident * cus),
+               &a.prefix_splits, &a.prefix_span);
+    const int64_t suffix_items = (int64_t)a.suffix_tiles * a.kv_heads * a.batch;
+    set_ranges(a.suffix, ranges_that_fill(a.suffix, suffix_items, resident * cus), &a.suffix_splits, &a.suffix_span);
 }
 
 int64_t part_bytes(const Args &a)
