@@ -37,8 +37,9 @@ constexpr int kRows = 16;      // rows of a tile
 constexpr int kStep = 32;      // keys of a step
 
 // What a launch's workgroups do: a prefix in 16-row tiles, or in 128-row
-// tiles (both with the sequences' own positions), or bounded caches.
-enum { kRowTiles, kTiles, kCache };
+// tiles (both with the sequences' own positions), or bounded caches in tiles
+// of 16 or of 128 rows.
+enum { kRowTiles, kTiles, kCache, kCacheTiles };
 
 struct Args {
     const uint16_t *q, *prefix_k, *prefix_v, *k, *v;
@@ -54,7 +55,7 @@ struct Args {
     float scale2;              // scale * log2(e)
     int32_t prefix_splits, prefix_span, prefix_tiles, suffix_splits, suffix_span, suffix_tiles;
     int64_t rows;              // batch * tokens * heads
-    bool big;                  // the prefix in 128-row tiles
+    bool big;                  // tiles of 128 rows
 };
 
 // The 32 keys from `base` on: rows in memory, and which of them which query
@@ -383,18 +384,39 @@ struct TileShape {
     }
 };
 
-template <class E, int DP>
-__device__ __forceinline__ void tile_block(const Args &a, char *lds, int head, int tile, int split)
+//
+// CACHE: the rows are one sequence's and the keys its cache's slots, each
+// with its place relative to the first query token (rel, as in Keys) in LDS
+// beside its key.
+template <class E, int DP, bool CACHE>
+__device__ __forceinline__ void tile_block(const Args &a, char *lds, int seq, int head, int tile, int split)
 {
     typedef TileShape<DP> S;
     constexpr int kKeys = S::kKeys;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31, g = lane >> 5;
-    const int row_count = a.batch * a.tokens * a.group;
-    const int n = a.prefix, key0 = split * a.prefix_span, key1 = min(n, key0 + a.prefix_span);
-    const uint16_t *kp = a.prefix_k + head * a.prefix_head, *vp = a.prefix_v + head * a.prefix_head;
+    const int row_count = (CACHE ? 1 : a.batch) * a.tokens * a.group;
+    const int n = CACHE ? max(0, min(a.lengths[seq], a.suffix)) : a.prefix;
+    const int span = CACHE ? a.suffix_span : a.prefix_span;
+    const int key0 = split * span, key1 = min(n, key0 + span);
+    if (key0 >= key1) return;
+    const int64_t kv_token = CACHE ? a.k_token : a.prefix_token;
+    const int64_t kv_from = CACHE ? seq * a.k_batch + head * a.k_head : head * a.prefix_head;
+    const uint16_t *kp = (CACHE ? a.k : a.prefix_k) + kv_from, *vp = (CACHE ? a.v : a.prefix_v) + kv_from;
+    const int32_t *places = CACHE ? a.positions + ((int64_t)seq * a.kv_heads + head) * a.suffix : nullptr;
+    const int pos = CACHE ? a.pos[seq] : 0;
+    // behind the two buffers: rel of each buffer's keys; whether a step has
+    // keys that not all tokens see (for three steps in turn); whether any of
+    // those had values that are no numbers
+    int32_t *const rels = (int32_t *)(lds + 2 * S::kBuffer);
+    int32_t *const mixed = rels + 2 * kKeys, *const odd = mixed + 3;
+    if (CACHE) {
+        if (threadIdx.x < 4) mixed[threadIdx.x] = 0;
+        __syncthreads();
+    }
 
     const int row = tile * kTileRows + wave * 32 + c;
-    const int t = row / a.group % a.tokens, b = row / (a.group * a.tokens), h = head * a.group + row % a.group;
+    const int t = row / a.group % a.tokens, h = head * a.group + row % a.group;
+    const int b = CACHE ? seq : row / (a.group * a.tokens);
     u32x4 q[DP / 16];
 #pragma unroll
     for (int i = 0; i < DP / 16; i++) {
@@ -407,35 +429,71 @@ __device__ __forceinline__ void tile_block(const Args &a, char *lds, int head, i
     // at a uniform address plus its own 32-bit distance.
     u32x4 kx[4], vx[4];
     const int v_quad = threadIdx.x / S::kChunks, v_chunk = threadIdx.x % S::kChunks;
-    const int32_t token = (int32_t)a.prefix_token;
+    const int32_t token = (int32_t)kv_token;
+    int32_t place[4];
     const int my_d = v_chunk * 8 < a.dim ? v_chunk * 8 : 0;
     const bool pad = v_chunk * 8 >= a.dim;   // dims that K does not have take part as 0
     const uint32_t k_far = (uint32_t)(v_quad * token) + my_d, v_far = (uint32_t)(4 * v_quad * token) + my_d;
     constexpr int kRowsEach = 256 / S::kChunks;   // keys between a thread's chunks of K
     const auto load = [&](int base) {
         if (base + kKeys <= key1) {
-            const uint16_t *k = kp + base * a.prefix_token, *v = vp + base * a.prefix_token;
+            const uint16_t *k = kp + base * kv_token, *v = vp + base * kv_token;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                kx[j] = *(const u32x4 *)(k + (int64_t)(kRowsEach * j) * a.prefix_token + k_far);
-                vx[j] = *(const u32x4 *)(v + j * a.prefix_token + v_far);
+                kx[j] = *(const u32x4 *)(k + (int64_t)(kRowsEach * j) * kv_token + k_far);
+                vx[j] = *(const u32x4 *)(v + j * kv_token + v_far);
+                if (CACHE) place[j] = places[base + 4 * v_quad + j];
             }
         } else {
             // the last step: keys past the end are 0
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 const int kk = base + kRowsEach * j + v_quad, kv = base + 4 * v_quad + j;
-                const u32x4 x = *(const u32x4 *)(kp + min(kk, n - 1) * a.prefix_token + my_d);
-                const u32x4 y = *(const u32x4 *)(vp + min(kv, n - 1) * a.prefix_token + my_d);
+                const u32x4 x = *(const u32x4 *)(kp + min(kk, n - 1) * kv_token + my_d);
+                const u32x4 y = *(const u32x4 *)(vp + min(kv, n - 1) * kv_token + my_d);
 #pragma unroll
                 for (int w = 0; w < 4; w++) kx[j][w] = kk < key1 ? x[w] : 0, vx[j][w] = kv < key1 ? y[w] : 0;
+                if (CACHE) place[j] = kv < key1 ? places[kv] : -1;
             }
         }
     };
     const int k_to = S::k_at(v_quad, v_chunk);
     // keys 4 w .. 4 w + 3 of a group of 16: half w / 2 of the chunk of lanes l / 32 = w % 2
     const int v_to = S::v_at(v_chunk * 8, v_quad / 4 * 2 + (v_quad & 1)) + (v_quad >> 1 & 1) * 8;
-    const auto store = [&](int buffer) {
+    const auto store = [&](int buffer, int turn) {
+        if (CACHE) {
+            int32_t rel[4];
+            bool some_not = false, no_number = false;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const bool some = place[j] >= 0 && (int64_t)place[j] <= (int64_t)pos + a.tokens - 1;
+                rel[j] = some ? place[j] - pos : 0x7fffffff;
+                some_not = some_not || rel[j] > 0;
+            }
+            // A value that a row does not see has weight 0 there, so it must
+            // be a number: those that no token sees are 0; those that some
+            // see are too, if they are no numbers, and come last (below).
+            if (some_not) {
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+#pragma unroll
+                    for (int w = 0; w < 4; w++) {
+                        const uint32_t x = vx[j][w];
+                        const bool low = (x & E::kExpMask) == E::kExpMask, high = (x >> 16 & E::kExpMask) == E::kExpMask;
+                        no_number = no_number || (rel[j] > 0 && rel[j] < a.tokens && (low || high));
+                        vx[j][w] = rel[j] >= a.tokens ? 0
+                                   : rel[j] <= 0      ? x
+                                                      : (low ? 0 : x & 0xffffu) | (high ? 0 : x & 0xffff0000u);
+                    }
+                mixed[turn] = 1;
+                if (no_number) *odd = 1;
+            }
+            if (v_chunk == 0)
+#pragma unroll
+                for (int j = 0; j < 4; j++) rels[(buffer ? kKeys : 0) + 4 * v_quad + j] = rel[j];
+            const int then = turn == 2 ? 0 : turn + 1;
+            if (threadIdx.x == 0) mixed[then] = 0;
+        }
         if (a.dim < DP) {
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -478,7 +536,9 @@ __device__ __forceinline__ void tile_block(const Args &a, char *lds, int head, i
         }
         return *(const u32x4 *)(lds + buffer + at);
     };
-    const auto step = [&](int buffer, int left) {
+    const auto step = [&](int buffer, int left, int turn) {
+        const bool some_not = CACHE && __builtin_amdgcn_readfirstlane(mixed[turn]);
+        const int32_t *const rel = rels + (buffer ? kKeys : 0);
         f32x16 s[kParts];
         u32x4 f[kFrags];
 #pragma unroll
@@ -498,7 +558,14 @@ __device__ __forceinline__ void tile_block(const Args &a, char *lds, int head, i
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
-        if (left < kKeys) {
+        if (some_not) {
+#pragma unroll
+            for (int k = 0; k < kParts; k++)
+#pragma unroll
+                for (int r = 0; r < 16; r++)
+                    if (rel[32 * k + 8 * (r / 4) + 4 * g + r % 4] > t) s[k][r] = -INFINITY;
+        }
+        if (!CACHE && left < kKeys) {
             __builtin_amdgcn_sched_barrier(0);   // a branch of its own: no step but the last pays for it
 #pragma unroll
             for (int k = 0; k < kParts; k++)
@@ -523,18 +590,22 @@ __device__ __forceinline__ void tile_block(const Args &a, char *lds, int head, i
             for (int i = 0; i < DP / 32; i++) o[i] *= by;
         }
         const float safe = m == -INFINITY ? 0.0f : m;
+        const auto weigh = [&](int k, int half) {
+            u32x4 pb;
+#pragma unroll
+            for (int w = 0; w < 4; w++) {
+                const float x = exp2_fast(__builtin_fmaf(s[k][8 * half + 2 * w], a.scale2, -safe));
+                const float y = exp2_fast(__builtin_fmaf(s[k][8 * half + 2 * w + 1], a.scale2, -safe));
+                l += x + y;
+                pb[w] = E::pack(x, y);
+            }
+            return pb;
+        };
 #pragma unroll
         for (int k = 0; k < kParts; k++)
 #pragma unroll
             for (int half = 0; half < 2; half++) {
-                u32x4 pb;
-#pragma unroll
-                for (int w = 0; w < 4; w++) {
-                    const float x = exp2_fast(__builtin_fmaf(s[k][8 * half + 2 * w], a.scale2, -safe));
-                    const float y = exp2_fast(__builtin_fmaf(s[k][8 * half + 2 * w + 1], a.scale2, -safe));
-                    l += x + y;
-                    pb[w] = E::pack(x, y);
-                }
+                const u32x4 pb = weigh(k, half);
 #pragma unroll
                 for (int i = 0; i < DP / 32; i++) {
                     const int at = kParts * kK + (2 * k + half) * (DP / 32) + i;
@@ -552,8 +623,9 @@ __device__ __forceinline__ void tile_block(const Args &a, char *lds, int head, i
     };
 
     load(key0);
-    store(0);
+    store(0, 0);
     __syncthreads();
+    int turn = 0;
     for (int base = key0; base < key1; base += 2 * kKeys) {
 #pragma unroll
         for (int half = 0; half < 2; half++) {
@@ -561,14 +633,47 @@ __device__ __forceinline__ void tile_block(const Args &a, char *lds, int head, i
             if (at >= key1) break;
             const bool more = at + kKeys < key1;
             if (more) load(at + kKeys);
-            step(half * S::kBuffer, key1 - at);
-            if (more) store((1 - half) * S::kBuffer);
+            step(half * S::kBuffer, key1 - at, turn);
+            turn = turn == 2 ? 0 : turn + 1;
+            if (more) store((1 - half) * S::kBuffer, turn);
             __syncthreads();
+        }
+    }
+    if (CACHE && *odd) {
+        // What was left out: each value that is no number and that only some
+        // tokens see, times its weight for the rows that do.
+        for (int base = key0; base < key1; base += 64) {
+            const int32_t at = base + lane < key1 ? places[base + lane] : -1;
+            const int32_t rel = at < 0 || at <= pos ? 0 : at - pos;
+            for (uint64_t left = __ballot(rel > 0 && rel < a.tokens); left; left &= left - 1) {
+                const int i = __builtin_ctzll(left);
+                const uint16_t *kr = kp + (base + i) * kv_token, *vr = vp + (base + i) * kv_token;
+                float x = 0.0f;
+#pragma unroll
+                for (int j = 0; j < DP / 16; j++)
+#pragma unroll
+                    for (int w = 0; w < 8; w++) {
+                        const int d = 16 * j + 8 * g + w;
+                        const uint32_t y = q[j][w / 2];
+                        if (d < a.dim) x += E::value(w & 1 ? y >> 16 : y & 0xffffu) * E::value(kr[d]);
+                    }
+                x += __shfl_xor(x, 32);
+                const bool sees = __shfl(rel, i) <= t;
+                const float p = exp2_fast(x * a.scale2 - (m == -INFINITY ? 0.0f : m));
+#pragma unroll
+                for (int j = 0; j < DP / 32; j++)
+#pragma unroll
+                    for (int r = 0; r < 16; r++) {
+                        const int d = 32 * j + 8 * (r / 4) + 4 * g + r % 4;
+                        const uint32_t y = d < a.dim ? vr[d] : 0;
+                        if (sees && (y & E::kExpMask) == E::kExpMask) o[j][r] += p * E::value(y);
+                    }
+            }
         }
     }
     l += __shfl_xor(l, 32);
     if (row < row_count) {
-        const int64_t out_row = ((int64_t)b * a.tokens + t) * a.heads + h;
+        const int64_t out_row = ((int64_t)b * a.tokens + t) * a.heads + h;   // (caches have no prefix ranges before theirs)
         float *to = a.part_o + (split * a.rows + out_row) * a.dim;
 #pragma unroll
         for (int i = 0; i < DP / 32; i++)
@@ -593,7 +698,18 @@ __global__ void __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) attend_kernel(
     typedef float JoinO[kRows][DP + 4];
     typedef float2 JoinMl[kRows];
     constexpr int kJoin = kWaves * (sizeof(JoinO) + sizeof(JoinMl));
-    __shared__ alignas(1024) char lds[KIND == kTiles && 2 * TileShape<DP>::kBuffer > kJoin ? 2 * TileShape<DP>::kBuffer : kJoin];
+    constexpr int kTile = 2 * TileShape<DP>::kBuffer + (KIND == kCacheTiles ? 8 * TileShape<DP>::kKeys + 16 : 0);
+    constexpr int kLds = KIND == kTiles ? (kTile > kJoin ? kTile : kJoin) : KIND == kCacheTiles ? kTile : kJoin;
+    __shared__ alignas(1024) char lds[kLds];
+    if constexpr (KIND == kCacheTiles) {
+        int item = blockIdx.x;
+        const int split = item % a.suffix_splits;
+        item /= a.suffix_splits;
+        const int tile = item % a.suffix_tiles;
+        item /= a.suffix_tiles;
+        tile_block<E, DP, true>(a, lds, item / a.kv_heads, item % a.kv_heads, tile, split);
+        return;
+    }
     JoinO *const join_o = (JoinO *)lds;
     JoinMl *const join_ml = (JoinMl *)(lds + kWaves * sizeof(JoinO));
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
@@ -603,7 +719,7 @@ __global__ void __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) attend_kernel(
     if constexpr (KIND == kTiles) {
         if (in_prefix) {
             split = item % a.prefix_splits, item /= a.prefix_splits;
-            tile_block<E, DP>(a, lds, item / a.prefix_tiles, item % a.prefix_tiles, split);
+            tile_block<E, DP, false>(a, lds, 0, item / a.prefix_tiles, item % a.prefix_tiles, split);
             return;
         }
     }
@@ -791,16 +907,105 @@ __device__ __forceinline__ void weigh_block(const Args &a, int bh, int first)
         if (key + j < n) to[j] += w[j];
 }
 
+// As weigh_block, from the logits taken again, where rows are many and their
+// logits would be more bytes than the keys: S = Q K^T with 32 rows of Q from
+// LDS against 32 keys of a wave, whose lanes l and l + 32 hold key l % 32's
+// logits with 32 rows between them.
+constexpr int kWeighRows = 128;
+
+template <class E, int DP>
+__device__ __forceinline__ void weigh_tiles(const Args &a, char *lds, int bh, int first)
+{
+    typedef TileShape<DP> S;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31, g = lane >> 5;
+    const int b = bh / a.kv_heads, head = bh % a.kv_heads;
+    const int n = max(0, min(a.lengths[b], a.suffix));
+    if (first >= n) return;
+    float *const top = (float *)(lds + kWeighRows * DP * 2);
+    int32_t *const token = (int32_t *)(top + kWeighRows);
+    const int row_count = a.tokens * a.group, parts = own_splits(a, b), pos = a.pos[b];
+    const uint16_t *kp = a.k + b * a.k_batch + head * a.k_head;
+    const int32_t *places = a.positions + (int64_t)bh * a.suffix;
+    float *weights = a.weights + (int64_t)bh * a.suffix;
+    for (int r0 = 0; r0 < row_count; r0 += kWeighRows) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < kWeighRows * S::kChunks; i += 64 * kWaves) {
+            const int r = i / S::kChunks, d = i % S::kChunks * 8, row = r0 + r;
+            const u32x4 x = row < row_count && d < a.dim
+                                ? *(const u32x4 *)(a.q + b * a.q_batch + row / a.group * a.q_token +
+                                                   (head * a.group + row % a.group) * a.q_head + d)
+                                : u32x4{0, 0, 0, 0};
+            *(u32x4 *)(lds + S::k_at(r, d / 8)) = x;
+        }
+        if (threadIdx.x < kWeighRows) {
+            const int row = r0 + threadIdx.x, t = row / a.group;
+            float m = -INFINITY, l = 0.0f;
+            if (row < row_count) {
+                const int64_t at = ((int64_t)b * a.tokens + t) * a.heads + head * a.group + row % a.group;
+#pragma unroll 4
+                for (int s = 0; s < parts; s++) m = fmaxf(m, a.part_ml[s * a.rows + at].x);
+                const float safe = m == -INFINITY ? 0.0f : m;
+#pragma unroll 4
+                for (int s = 0; s < parts; s++) {
+                    const float2 x = a.part_ml[s * a.rows + at];
+                    l += exp2_fast(x.x - safe) * x.y;
+                }
+            }
+            top[threadIdx.x] = l == 0.0f ? INFINITY : m + __log2f(l);   // an empty row gives nothing
+            token[threadIdx.x] = row < row_count ? t : -0x7fffffff;
+        }
+        __syncthreads();
+        for (int base = first + 32 * wave; base < min(n, first + kWeighKeys); base += 32 * kWaves) {
+            const int key = min(base + c, n - 1);
+            u32x4 kx[DP / 16];
+#pragma unroll
+            for (int i = 0; i < DP / 16; i++) {
+                const int d = 16 * i + 8 * g;
+                kx[i] = d < a.dim ? *(const u32x4 *)(kp + key * a.k_token + d) : u32x4{0, 0, 0, 0};
+            }
+            const int32_t place = base + c < n ? places[key] : -1;
+            const bool some = place >= 0 && (int64_t)place <= (int64_t)pos + a.tokens - 1;
+            const int32_t rel = some ? place - pos : 0x7fffffff;
+            const bool mixed = __any(rel > 0);
+            float w = 0.0f;
+            for (int r = 0; r < min(kWeighRows, row_count - r0); r += 32) {
+                f32x16 s;
+#pragma unroll
+                for (int i = 0; i < 16; i++) s[i] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < DP / 16; i++)
+                    s = E::mfma32(*(const u32x4 *)(lds + S::k_at(r + c, 2 * i + g)), kx[i], s);
+                const bool all = !mixed && r0 + r + 32 <= row_count;
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const int at = r + 2 * i + 4 * g;
+                    const f32x4 x = *(const f32x4 *)(top + at);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const float p = exp2_fast(__builtin_fmaf(s[i + j], a.scale2, -x[j]));
+                        w += all || rel <= token[at + j] ? p : 0.0f;
+                    }
+                }
+            }
+            w += __shfl_xor(w, 32);
+            if (g == 0 && some) weights[key] += w;
+        }
+    }
+}
+
 // Workgroups below the number of output rows join one row each; behind them
 // those of bounded caches add up the slots' weights.
-template <class E, int KIND>
+template <class E, int DP, int KIND>
 __global__ void __launch_bounds__(64 * kWaves) finish_kernel(const Args a)
 {
-    if (KIND != kCache || blockIdx.x < a.rows) {
+    __shared__ alignas(1024) char lds[KIND == kCacheTiles ? kWeighRows * (DP * 2 + 8) : 16];
+    if ((KIND != kCache && KIND != kCacheTiles) || blockIdx.x < a.rows) {
         join_block<E>(a, blockIdx.x);
     } else {
         const int runs = (a.suffix + kWeighKeys - 1) / kWeighKeys, item = blockIdx.x - (int)a.rows;
-        weigh_block(a, item / runs, item % runs * kWeighKeys);
+        const int bh = item / runs, first = item % runs * kWeighKeys;
+        if constexpr (KIND == kCacheTiles) weigh_tiles<E, DP>(a, lds, bh, first);
+        else weigh_block(a, bh, first);
     }
 }
 
@@ -831,16 +1036,16 @@ int64_t ranges_that_fill(int64_t keys, int64_t items, int64_t slots)
     return best;
 }
 
-void plan(Args &a)
+void plan(Args &a, bool cache)
 {
     const int64_t cus = df11::cu_count();
     const int64_t resident = a.dim <= 64 ? 3 : a.dim <= 128 ? 2 : 1;   // workgroups of a CU, by the kernels' registers
     a.rows = (int64_t)a.batch * a.tokens * a.heads;
     if (!a.rows) return;
-    const int64_t shared_rows = (int64_t)a.batch * a.tokens * a.group;
-    a.big = shared_rows > 32;
+    const int64_t own_rows = (int64_t)a.tokens * a.group, shared_rows = a.batch * own_rows;
+    a.big = (cache ? own_rows : shared_rows) > 32;
     a.prefix_tiles = ceil_div(shared_rows, a.big ? kTileRows : kRows);
-    a.suffix_tiles = ceil_div((int64_t)a.tokens * a.group, kRows);
+    a.suffix_tiles = ceil_div(own_rows, cache && a.big ? kTileRows : kRows);
     // 128-row tiles: one workgroup on each CU, whose partial sums are few and
     // which leaves room for those of the sequences' own positions; two where
     // a long prefix is nearly all there is (128 requests behind 32768
@@ -889,25 +1094,32 @@ int strides_ok(const char *who, std::initializer_list<int64_t> strides, std::ini
     return DF11_OK;
 }
 
-template <class E, int KIND>
+template <class E, int DP, int KIND>
 int launch(const Args &a, hipStream_t st)
 {
-    constexpr bool CACHE = KIND == kCache;
+    constexpr bool CACHE = KIND == kCache || KIND == kCacheTiles;
     const int64_t items = (CACHE ? 0 : (int64_t)a.kv_heads * a.prefix_tiles * a.prefix_splits) +
                           (int64_t)a.batch * a.kv_heads * a.suffix_tiles * a.suffix_splits;
-    if (items > 0x7fffffffll) return df11::fail(DF11_E_ARG, "attention: too many rows and keys for one launch");
-    const dim3 grid((uint32_t)items), block(64 * kWaves);
-    if (items) {
-        if (a.dim <= 64) hipLaunchKernelGGL((attend_kernel<E, 64, KIND>), grid, block, 0, st, a);
-        else if (a.dim <= 128) hipLaunchKernelGGL((attend_kernel<E, 128, KIND>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((attend_kernel<E, 256, KIND>), grid, block, 0, st, a);
-    }
     const int64_t finish = a.rows + (CACHE ? (int64_t)a.batch * a.kv_heads * ceil_div(a.suffix, kWeighKeys) : 0);
-    if (finish > 0x7fffffffll) return df11::fail(DF11_E_ARG, "attention: too many rows and slots for one launch");
-    hipLaunchKernelGGL((finish_kernel<E, KIND>), dim3((uint32_t)finish), block, 0, st, a);
+    if (items > 0x7fffffffll || finish > 0x7fffffffll)
+        return df11::fail(DF11_E_ARG, "attention: too many rows and keys for one launch");
+    const dim3 block(64 * kWaves);
+    if (items) hipLaunchKernelGGL((attend_kernel<E, DP, KIND>), dim3((uint32_t)items), block, 0, st, a);
+    constexpr int JOIN = KIND == kTiles ? kRowTiles : KIND;   // a prefix's sums are joined alike
+    hipLaunchKernelGGL((finish_kernel<E, KIND == kCacheTiles ? DP : 64, JOIN>), dim3((uint32_t)finish), block, 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return df11::fail(DF11_E_DEVICE, "attention launch: %s", hipGetErrorString(e));
     return DF11_OK;
+}
+
+template <int KIND>
+int launch_kind(const Args &a, int64_t dtype, hipStream_t st)
+{
+    if (dtype == DF11_FP16)
+        return a.dim <= 64 ? launch<Fp16, 64, KIND>(a, st) : a.dim <= 128 ? launch<Fp16, 128, KIND>(a, st)
+                                                                         : launch<Fp16, 256, KIND>(a, st);
+    return a.dim <= 64 ? launch<Bf16, 64, KIND>(a, st) : a.dim <= 128 ? launch<Bf16, 128, KIND>(a, st)
+                                                                     : launch<Bf16, 256, KIND>(a, st);
 }
 
 int check_workspace(const char *who, void *ws, uint64_t bytes, uint64_t need)
@@ -953,7 +1165,7 @@ int make_prefix(const df11_prefix_attention_args *p, Args &a)
     a.k_batch = p->k_batch, a.k_token = p->k_token, a.k_head = p->k_head, a.table_batch = p->table_batch;
     a.scale2 = (float)(p->scale * 1.44269504088896340736);
     if (!(a.scale2 > 0.0f && a.scale2 < INFINITY)) return df11::fail(DF11_E_ARG, "%s: scale must be positive", who);
-    plan(a);
+    plan(a, false);
     return DF11_OK;
 }
 
@@ -978,8 +1190,8 @@ int make_cache(const df11_cache *c, const df11_cache_attention_args *p, Args &a)
     a.k_batch = c->stride_batch, a.k_token = c->stride_slot, a.k_head = c->stride_head;
     a.scale2 = (float)(p->scale * 1.44269504088896340736);
     if (!(a.scale2 > 0.0f && a.scale2 < INFINITY)) return df11::fail(DF11_E_ARG, "%s: scale must be positive", who);
-    plan(a);
-    a.logit_stride = (c->slots + 31) / 32 * 32;
+    plan(a, true);
+    a.logit_stride = a.big ? 0 : (c->slots + 31) / 32 * 32;   // many rows: taken again, not kept
     return DF11_OK;
 }
 
@@ -1010,9 +1222,8 @@ extern "C" int df11_prefix_attention(const df11_prefix_attention_args *p, void *
     rc = check_workspace(who, workspace, workspace_bytes, part_bytes(a));
     if (rc) return rc;
     place(a, workspace);
-    hipStream_t st = (hipStream_t)stream;
-    if (a.big) return p->dtype == DF11_FP16 ? launch<Fp16, kTiles>(a, st) : launch<Bf16, kTiles>(a, st);
-    return p->dtype == DF11_FP16 ? launch<Fp16, kRowTiles>(a, st) : launch<Bf16, kRowTiles>(a, st);
+    return a.big ? launch_kind<kTiles>(a, p->dtype, (hipStream_t)stream)
+                 : launch_kind<kRowTiles>(a, p->dtype, (hipStream_t)stream);
 }
 
 extern "C" uint64_t df11_cache_attention_workspace_bytes(const df11_cache *c, const df11_cache_attention_args *p)
@@ -1035,6 +1246,6 @@ extern "C" int df11_cache_attention(const df11_cache *c, const df11_cache_attent
     rc = check_workspace(who, workspace, workspace_bytes, cache_bytes(a));
     if (rc) return rc;
     place(a, workspace);
-    return c->dtype == DF11_FP16 ? launch<Fp16, kCache>(a, (hipStream_t)stream)
-                                 : launch<Bf16, kCache>(a, (hipStream_t)stream);
+    return a.big ? launch_kind<kCacheTiles>(a, c->dtype, (hipStream_t)stream)
+                 : launch_kind<kCache>(a, c->dtype, (hipStream_t)stream);
 }

@@ -25,6 +25,7 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // from float32 (to nearest, ties to even) and the bits of a non-finite value.
 struct Bf16 {
     static constexpr uint32_t kExpMask = 0x7f80u;
+    static __device__ __forceinline__ float value(uint32_t x) { return __builtin_bit_cast(float, x << 16); }
     static __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
@@ -43,6 +44,7 @@ struct Bf16 {
 
 struct Fp16 {
     static constexpr uint32_t kExpMask = 0x7c00u;
+    static __device__ __forceinline__ float value(uint32_t x) { return (float)__builtin_bit_cast(_Float16, (uint16_t)x); }
     static __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,

@@ -206,7 +206,7 @@ def _cuda_cache(x):
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("B,T,C,Hq,H,D", [
     (1, 1, 1, 1, 1, 8), (2, 1, 33, 8, 2, 128), (3, 1, 300, 4, 4, 64), (2, 5, 129, 6, 2, 96), (1, 20, 260, 8, 1, 128),
-    (2, 1, 1500, 7, 1, 256), (2, 2, 64, 40, 2, 80)])
+    (2, 1, 1500, 7, 1, 256), (2, 2, 64, 40, 2, 80), (2, 33, 2100, 8, 2, 128), (1, 70, 1030, 4, 1, 256), (3, 40, 90, 2, 2, 64)])
 def test_cache_attention(B, T, C, Hq, H, D, dtype):
     print("case", (B, T, C, Hq, H, D, dtype), flush=True)
     x = _cache_case(B + C + D, B, H, C, D, [C - (i * C) // (2 * B) for i in range(B)], dtype, more=9)
@@ -255,6 +255,37 @@ def test_cache_attention_later_tokens_do_not_reach_earlier_ones():
     out = serve.cache_attention(q.cuda(), c, pos.cuda())
     _close(out[:, :2], want[:, :2], bound[:, :2], "earlier tokens")
     assert bool(torch.isnan(out[:, 2]).all())
+    _close(c.weights, want_w, 2.0 ** -12 * (want_w - x["weights"].double()) + 2.0 ** -22 * want_w, "weights")
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("T,Hq,H,D,C", [(24, 4, 2, 128, 300), (40, 1, 1, 64, 150), (33, 4, 4, 256, 70), (9, 8, 2, 72, 129)])
+def test_cache_attention_window_with_values_that_are_no_numbers(T, Hq, H, D, C, bad, dtype):
+    """Many rows: the three last positions' values, and every unseen slot, hold `bad`."""
+    x = _cache_case(T + D, 2, H, C, D, [C, C - 5], dtype, more=4)
+    pos = torch.tensor([C + 4 - T, C - 10 - T], dtype=torch.int32)
+    clean = {n: t.clone() for n, t in x.items()}
+    first_bad = []
+    for b in range(2):
+        last = int(pos[b]) + T - 1
+        unseen = (torch.arange(C) >= x["lengths"][b]) | (x["positions"][b] > last)
+        late = ~unseen & (x["positions"][b] > last - 3)
+        x["k"][b][unseen] = bad
+        x["v"][b][unseen | late] = bad
+        clean["k"][b][unseen] = 0
+        clean["v"][b][unseen | late] = 0
+        first_bad.append([T - 3 + int(3 - 1 - (last - x["positions"][b, h][late[h]]).max()) if late[h].any() else T
+                          for h in range(H)])
+    q = _randn(_gen(T), 2, T, Hq, D, dtype=dtype)
+    want, want_w, bound = ref.cache_attention(q, pos=pos, **clean)
+    c = _cuda_cache(x)
+    out = serve.cache_attention(q.cuda(), c, pos.cuda()).cpu()
+    for b in range(2):
+        for h in range(H):
+            heads, t = slice(h * (Hq // H), (h + 1) * (Hq // H)), first_bad[b][h]
+            _close(out[b, :t, heads], want[b, :t, heads], bound[b, :t, heads], (b, h))
+            assert not bool(torch.isfinite(out[b, t:, heads]).any())
     _close(c.weights, want_w, 2.0 ** -12 * (want_w - x["weights"].double()) + 2.0 ** -22 * want_w, "weights")
 
 
