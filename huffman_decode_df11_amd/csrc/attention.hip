@@ -48,7 +48,8 @@ struct Args {
     float *lse, *weights;
     float *part_o;             // [slot][row][dim]
     float2 *part_ml;           // [slot][row]
-    float *logits;             // cache: [batch * kv_heads][rows of a head][logit_stride]
+    float *tops;               // many rows of a cache: a row's logarithm (base 2) of its sum, +infinity if it is empty
+    float *logits;             // few rows: [batch * kv_heads][rows of a head][logit_stride]
     int32_t batch, tokens, heads, kv_heads, group, dim, prefix, suffix, page, n_pages, fp16;
     int64_t q_batch, q_token, q_head, prefix_token, prefix_head, k_batch, k_token, k_head, table_batch;
     int64_t logit_stride;
@@ -866,7 +867,11 @@ __device__ __forceinline__ void join_block(const Args &a, int64_t row)
         for (int w = 0; w < kWaves; w++) x += sums[w][threadIdx.x].x, y += sums[w][threadIdx.x].y;
         *(uint32_t *)(a.out + row * a.dim + 2 * threadIdx.x) = E::pack(x * inv, y * inv);
     }
-    if (a.lse && threadIdx.x == 0) a.lse[row] = ml.y == 0.0f ? -INFINITY : kLn2 * (ml.x + __log2f(ml.y));
+    if (threadIdx.x == 0) {
+        const float top = ml.x + __log2f(ml.y);
+        if (a.lse) a.lse[row] = ml.y == 0.0f ? -INFINITY : kLn2 * top;
+        if (a.tops) a.tops[row] = ml.y == 0.0f ? INFINITY : top;   // an empty row gives no slot anything
+    }
 }
 
 constexpr int kWeighKeys = 1024;   // slots of a workgroup, four to a thread
@@ -912,18 +917,21 @@ __device__ __forceinline__ void weigh_block(const Args &a, int bh, int first)
 // LDS against 32 keys of a wave, whose lanes l and l + 32 hold key l % 32's
 // logits with 32 rows between them.
 constexpr int kWeighRows = 128;
+constexpr int kTileKeys = 512;   // slots of a workgroup
 
 template <class E, int DP>
-__device__ __forceinline__ void weigh_tiles(const Args &a, char *lds, int bh, int first)
+__global__ void __launch_bounds__(64 * kWaves, 2) weigh_kernel(const Args a)
 {
     typedef TileShape<DP> S;
+    __shared__ alignas(1024) char lds[kWeighRows * (DP * 2 + 8)];
+    const int bh = blockIdx.y, first = blockIdx.x * kTileKeys;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31, g = lane >> 5;
     const int b = bh / a.kv_heads, head = bh % a.kv_heads;
     const int n = max(0, min(a.lengths[b], a.suffix));
     if (first >= n) return;
     float *const top = (float *)(lds + kWeighRows * DP * 2);
     int32_t *const token = (int32_t *)(top + kWeighRows);
-    const int row_count = a.tokens * a.group, parts = own_splits(a, b), pos = a.pos[b];
+    const int row_count = a.tokens * a.group, pos = a.pos[b];
     const uint16_t *kp = a.k + b * a.k_batch + head * a.k_head;
     const int32_t *places = a.positions + (int64_t)bh * a.suffix;
     float *weights = a.weights + (int64_t)bh * a.suffix;
@@ -938,53 +946,67 @@ __device__ __forceinline__ void weigh_tiles(const Args &a, char *lds, int bh, in
             *(u32x4 *)(lds + S::k_at(r, d / 8)) = x;
         }
         if (threadIdx.x < kWeighRows) {
-            const int row = r0 + threadIdx.x, t = row / a.group;
-            float m = -INFINITY, l = 0.0f;
-            if (row < row_count) {
-                const int64_t at = ((int64_t)b * a.tokens + t) * a.heads + head * a.group + row % a.group;
-#pragma unroll 4
-                for (int s = 0; s < parts; s++) m = fmaxf(m, a.part_ml[s * a.rows + at].x);
-                const float safe = m == -INFINITY ? 0.0f : m;
-#pragma unroll 4
-                for (int s = 0; s < parts; s++) {
-                    const float2 x = a.part_ml[s * a.rows + at];
-                    l += exp2_fast(x.x - safe) * x.y;
-                }
-            }
-            top[threadIdx.x] = l == 0.0f ? INFINITY : m + __log2f(l);   // an empty row gives nothing
-            token[threadIdx.x] = row < row_count ? t : -0x7fffffff;
+            const int row = r0 + threadIdx.x, at = row / a.group;
+            const bool there = row < row_count;
+            top[threadIdx.x] =
+                there ? a.tops[((int64_t)b * a.tokens + at) * a.heads + head * a.group + row % a.group] : INFINITY;
+            token[threadIdx.x] = there ? at : -0x7fffffff;
         }
         __syncthreads();
-        for (int base = first + 32 * wave; base < min(n, first + kWeighKeys); base += 32 * kWaves) {
+        const int q_from = S::k_at(c, g);
+        u32x4 kx[DP / 16], next[DP / 16];
+        int32_t place, next_place;
+        const auto load = [&](int base) {
             const int key = min(base + c, n - 1);
-            u32x4 kx[DP / 16];
 #pragma unroll
             for (int i = 0; i < DP / 16; i++) {
                 const int d = 16 * i + 8 * g;
-                kx[i] = d < a.dim ? *(const u32x4 *)(kp + key * a.k_token + d) : u32x4{0, 0, 0, 0};
+                next[i] = d < a.dim ? *(const u32x4 *)(kp + key * a.k_token + d) : u32x4{0, 0, 0, 0};
             }
-            const int32_t place = base + c < n ? places[key] : -1;
+            next_place = base + c < n ? places[key] : -1;
+        };
+        const int end = min(n, first + kTileKeys);
+        load(first + 32 * wave);
+        for (int base = first + 32 * wave; base < end; base += 32 * kWaves) {
+            const int key = base + c;
+#pragma unroll
+            for (int i = 0; i < DP / 16; i++) kx[i] = next[i];
+            place = next_place;
+            if (base + 32 * kWaves < end) load(base + 32 * kWaves);
             const bool some = place >= 0 && (int64_t)place <= (int64_t)pos + a.tokens - 1;
             const int32_t rel = some ? place - pos : 0x7fffffff;
             const bool mixed = __any(rel > 0);
             float w = 0.0f;
-            for (int r = 0; r < min(kWeighRows, row_count - r0); r += 32) {
-                f32x16 s;
+            // two tiles of 32 rows at a time, whose products do not wait for each other
+            for (int r = 0; r < min(kWeighRows, row_count - r0); r += 64) {
+                f32x16 s[2];
 #pragma unroll
-                for (int i = 0; i < 16; i++) s[i] = 0.0f;
+                for (int k = 0; k < 2; k++)
+#pragma unroll
+                    for (int i = 0; i < 16; i++) s[k][i] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < DP / 16; i++)
-                    s = E::mfma32(*(const u32x4 *)(lds + S::k_at(r + c, 2 * i + g)), kx[i], s);
-                const bool all = !mixed && r0 + r + 32 <= row_count;
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const int at = r + 2 * i + 4 * g;
-                    const f32x4 x = *(const f32x4 *)(top + at);
+                    for (int k = 0; k < 2; k++)
+                        s[k] = E::mfma32(*(const u32x4 *)(lds + S::k_next(q_from, i) + (r + 32 * k) * DP * 2), kx[i], s[k]);
+                f32x4 x[2][4];
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const float p = exp2_fast(__builtin_fmaf(s[i + j], a.scale2, -x[j]));
-                        w += all || rel <= token[at + j] ? p : 0.0f;
-                    }
+                for (int k = 0; k < 2; k++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) x[k][i] = *(const f32x4 *)(top + r + 32 * k + 8 * i + 4 * g);
+                if (!mixed && r0 + r + 64 <= row_count) {
+#pragma unroll
+                    for (int k = 0; k < 2; k++)
+#pragma unroll
+                        for (int i = 0; i < 16; i++) w += exp2_fast(__builtin_fmaf(s[k][i], a.scale2, -x[k][i / 4][i % 4]));
+                } else {
+                    for (int k = 0; k < 2; k++)
+#pragma unroll
+                        for (int i = 0; i < 16; i++) {
+                            const float p = exp2_fast(__builtin_fmaf(s[k][i], a.scale2, -x[k][i / 4][i % 4]));
+                            const int32_t last = token[r + 32 * k + 8 * (i / 4) + 4 * g + i % 4];
+                            w += rel <= last ? p : 0.0f;
+                        }
                 }
             }
             w += __shfl_xor(w, 32);
@@ -995,17 +1017,14 @@ __device__ __forceinline__ void weigh_tiles(const Args &a, char *lds, int bh, in
 
 // Workgroups below the number of output rows join one row each; behind them
 // those of bounded caches add up the slots' weights.
-template <class E, int DP, int KIND>
+template <class E, bool WEIGH>
 __global__ void __launch_bounds__(64 * kWaves) finish_kernel(const Args a)
 {
-    __shared__ alignas(1024) char lds[KIND == kCacheTiles ? kWeighRows * (DP * 2 + 8) : 16];
-    if ((KIND != kCache && KIND != kCacheTiles) || blockIdx.x < a.rows) {
+    if (!WEIGH || blockIdx.x < a.rows) {
         join_block<E>(a, blockIdx.x);
     } else {
         const int runs = (a.suffix + kWeighKeys - 1) / kWeighKeys, item = blockIdx.x - (int)a.rows;
-        const int bh = item / runs, first = item % runs * kWeighKeys;
-        if constexpr (KIND == kCacheTiles) weigh_tiles<E, DP>(a, lds, bh, first);
-        else weigh_block(a, bh, first);
+        weigh_block(a, item / runs, item % runs * kWeighKeys);
     }
 }
 
@@ -1100,13 +1119,17 @@ int launch(const Args &a, hipStream_t st)
     constexpr bool CACHE = KIND == kCache || KIND == kCacheTiles;
     const int64_t items = (CACHE ? 0 : (int64_t)a.kv_heads * a.prefix_tiles * a.prefix_splits) +
                           (int64_t)a.batch * a.kv_heads * a.suffix_tiles * a.suffix_splits;
-    const int64_t finish = a.rows + (CACHE ? (int64_t)a.batch * a.kv_heads * ceil_div(a.suffix, kWeighKeys) : 0);
+    const int64_t finish =
+        a.rows + (KIND == kCache ? (int64_t)a.batch * a.kv_heads * ceil_div(a.suffix, kWeighKeys) : 0);
     if (items > 0x7fffffffll || finish > 0x7fffffffll)
         return df11::fail(DF11_E_ARG, "attention: too many rows and keys for one launch");
     const dim3 block(64 * kWaves);
     if (items) hipLaunchKernelGGL((attend_kernel<E, DP, KIND>), dim3((uint32_t)items), block, 0, st, a);
-    constexpr int JOIN = KIND == kTiles ? kRowTiles : KIND;   // a prefix's sums are joined alike
-    hipLaunchKernelGGL((finish_kernel<E, KIND == kCacheTiles ? DP : 64, JOIN>), dim3((uint32_t)finish), block, 0, st, a);
+    hipLaunchKernelGGL((finish_kernel<E, KIND == kCache>), dim3((uint32_t)finish), block, 0, st, a);
+    if constexpr (KIND == kCacheTiles) {
+        const dim3 grid(ceil_div(a.suffix, kTileKeys), a.batch * a.kv_heads);
+        if (a.suffix) hipLaunchKernelGGL((weigh_kernel<E, DP>), grid, block, 0, st, a);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return df11::fail(DF11_E_DEVICE, "attention launch: %s", hipGetErrorString(e));
     return DF11_OK;
@@ -1135,7 +1158,9 @@ void place(Args &a, void *ws)
     const int64_t slots = a.prefix_splits + a.suffix_splits;
     a.part_o = (float *)ws;
     a.part_ml = (float2 *)(a.part_o + slots * a.rows * a.dim);
-    a.logits = (float *)((char *)ws + (part_bytes(a) + 15) / 16 * 16);
+    float *more = (float *)((char *)ws + (part_bytes(a) + 15) / 16 * 16);
+    if (a.positions && a.big) a.tops = more;
+    else if (a.positions) a.logits = more;
 }
 
 int make_prefix(const df11_prefix_attention_args *p, Args &a)
@@ -1197,7 +1222,7 @@ int make_cache(const df11_cache *c, const df11_cache_attention_args *p, Args &a)
 
 uint64_t cache_bytes(const Args &a)
 {
-    return (part_bytes(a) + 15) / 16 * 16 + 4ull * a.batch * a.kv_heads * a.tokens * a.group * a.logit_stride;
+    return (part_bytes(a) + 15) / 16 * 16 + 4ull * a.rows * (a.big ? 1 : a.logit_stride);
 }
 
 }  // namespace
