@@ -27,12 +27,13 @@ struct Args {
     int32_t token_bytes, batch, drafts, vocab;
     int64_t target_batch, target_row, draft_batch, draft_row;
     int32_t parts;
-    u64 *sums;   // [batch][parts][2]
+    u64 *sums;       // [batch][parts][2]
+    int32_t *taken;  // [batch]
 };
 
 constexpr int kThreads = 256;
-constexpr int kRun = 8;                          // tokens a thread holds in the last search
-constexpr int kPiece = kThreads * kRun * 4;      // tokens of a part: 2^13, so that a part's sum is below 2^53
+constexpr int kRun = 32;                         // tokens a thread holds in the last search
+constexpr int kPiece = kThreads * kRun;          // tokens of a part: 2^13, so that a part's sum is below 2^53
 
 struct F32 {
     typedef float type;
@@ -180,6 +181,7 @@ __global__ void __launch_bounds__(kThreads) part_kernel(const Args a)
     const int part = blockIdx.x, b = blockIdx.y;
     const int count = a.counts ? max(0, min(a.counts[b], a.drafts)) : a.drafts;
     const int n = drafts_taken<T>(a, b, count, &first_refused);
+    if (part == 0 && threadIdx.x == 0) a.taken[b] = n;
     u64 rest, all;
     part_sums<T>(rows_of<T>(a, b, count, n), part * kPiece, min(a.vocab, (part + 1) * kPiece), lds, rest, all);
     if (threadIdx.x == 0) {
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(kThreads) draw_kernel(const Args a)
     __shared__ int first_refused, chosen, drawn;
     const int b = blockIdx.x;
     const int count = a.counts ? max(0, min(a.counts[b], a.drafts)) : a.drafts;
-    const int n = drafts_taken<T>(a, b, count, &first_refused);
+    const int n = a.parts > 1 ? a.taken[b] : drafts_taken<T>(a, b, count, &first_refused);
     Rows<T> r = rows_of<T>(a, b, count, n);
     const float last = a.uniforms[(int64_t)b * (a.drafts + 1) + a.drafts];
     const u64 u = (u64)(fminf(fmaxf(last, 0.0f), 0.99999994f) * 16777216.0f);
@@ -236,34 +238,42 @@ __global__ void __launch_bounds__(kThreads) draw_kernel(const Args a)
         }
     }
     __syncthreads();
-    u64 start = before_part;
-    const int part = chosen;
-    // the part in rounds of kRun tokens a thread
-    for (int i0 = part * kPiece; i0 < min(a.vocab, (part + 1) * kPiece); i0 += kThreads * kRun) {
-        const int first = i0 + threadIdx.x * kRun;
-        double x[kRun], sum = 0.0;
+    // the part, kRun tokens in a row to a thread
+    const int part = chosen, first = part * kPiece + threadIdx.x * kRun;
+    typedef typename T::type type;
+    constexpr int V = 16 / sizeof(type);
+    type p[kRun], q[kRun];
+#pragma unroll
+    for (int v = 0; v < kRun; v += V) {
+        if (first + v + V <= a.vocab) {
+            __builtin_memcpy(p + v, r.p + first + v, 16);
+            if (r.q) __builtin_memcpy(q + v, r.q + first + v, 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                const int i = first + v + j;
+                p[v + j] = i < a.vocab ? r.p[i] : 0;
+                if (r.q) q[v + j] = i < a.vocab ? r.q[i] : 0;
+            }
+        }
+    }
+    const auto weight = [&](int j) {
+        const double x = whole(T::value(p[j]));
+        return r.rest ? r.left(x, r.q ? whole(T::value(q[j])) : r.refused(first + j)) : x;
+    };
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < kRun; j++) sum += weight(j);
+    u64 s = before_part + sum_before((u64)sum, lds);
+    if (s <= goal && goal < s + (u64)sum) {
 #pragma unroll
         for (int j = 0; j < kRun; j++) {
-            const int i = first + j;
-            x[j] = 0.0;
-            if (i < a.vocab) {
-                x[j] = whole(T::value(r.p[i]));
-                if (r.rest) x[j] = r.left(x[j], r.q ? whole(T::value(r.q[i])) : r.refused(i));
-            }
-            sum += x[j];
+            const u64 x = (u64)weight(j);
+            if (s <= goal && goal < s + x) drawn = first + j;
+            s += x;
         }
-        u64 s = start + sum_before((u64)sum, lds);
-        if (s <= goal && goal < s + (u64)sum) {
-#pragma unroll
-            for (int j = 0; j < kRun; j++) {
-                if (s <= goal && goal < s + (u64)x[j]) drawn = first + j;
-                s += (u64)x[j];
-            }
-        }
-        for (int w = 0; w < kThreads / 64; w++) start += lds[w];
-        __syncthreads();
-        if (drawn >= 0) break;
     }
+    __syncthreads();
     for (int i = threadIdx.x; i <= a.drafts; i += kThreads) {
         const int64_t at = (int64_t)b * (a.drafts + 1) + i;
         put(a.tokens, a.token_bytes, at,
@@ -298,16 +308,19 @@ int check(const df11_verify_args *p, Args &a)
     a = Args{p->draft_tokens, p->counts, (const uint8_t *)p->target_probs, (const uint8_t *)p->draft_probs, p->uniforms,
              p->tokens, p->accepted, (int32_t)p->token_bytes, (int32_t)p->batch, (int32_t)p->drafts, (int32_t)p->vocab,
              p->target_batch, p->target_row, p->draft_batch, p->draft_row,
-             (int32_t)((p->vocab + kPiece - 1) / kPiece), nullptr};
+             (int32_t)((p->vocab + kPiece - 1) / kPiece), nullptr, nullptr};
     return DF11_OK;
 }
+
+// A vocabulary of one part needs none.
+uint64_t workspace_of(const Args &a) { return a.parts > 1 ? 16ull * a.batch * a.parts + 4ull * a.batch : 0; }
 
 }  // namespace
 
 extern "C" uint64_t df11_verify_drafts_workspace_bytes(const df11_verify_args *p)
 {
     Args a;
-    return check(p, a) || a.parts == 1 ? 0 : 16ull * a.batch * a.parts;
+    return check(p, a) ? 0 : workspace_of(a);
 }
 
 extern "C" int df11_verify_drafts(const df11_verify_args *p, void *workspace, uint64_t workspace_bytes, void *stream)
@@ -321,11 +334,12 @@ extern "C" int df11_verify_drafts(const df11_verify_args *p, void *workspace, ui
     if (!a.target || ((uintptr_t)a.target & mask) || ((uintptr_t)a.draft & mask) || !a.uniforms || !a.tokens ||
         !a.accepted || (a.drafts && !a.draft_tokens))
         return df11::fail(DF11_E_ARG, "%s: null or misaligned pointer", who);
-    const uint64_t need = a.parts > 1 ? 16ull * a.batch * a.parts : 0;
+    const uint64_t need = workspace_of(a);
     if (workspace_bytes < need || (need && !aligned16(workspace)))
         return df11::fail(DF11_E_ARG, "%s: the workspace must be 16-byte aligned and hold %llu bytes", who,
                           (unsigned long long)need);
     a.sums = (u64 *)workspace;
+    a.taken = (int32_t *)(a.sums + 2ll * a.batch * a.parts);
     hipStream_t st = (hipStream_t)stream;
     return p->dtype == DF11_FP32 ? launch<F32>(a, st) : p->dtype == DF11_BF16 ? launch<BF>(a, st) : launch<HF>(a, st);
 }

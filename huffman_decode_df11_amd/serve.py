@@ -37,43 +37,44 @@ _CACHE_ARGS = struct.Struct("8qd")
 _VERIFY_ARGS = struct.Struct("16q")
 
 
-def _same(name: str, t, dtype, device) -> None:
+# The checks of a call's tensors: one condition that holds where all is well,
+# and behind it what names the fault.
+def _fault(name: str, t, dtype, device, shape) -> None:
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.device != device:
         raise ValueError("%s is on %s, the other operands on %s" % (name, t.device, device))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
 
 
 def _flat(name: str, t, dtype, device, shape) -> int:
     """The address of a contiguous tensor of this type, device and shape."""
-    if t.dtype != dtype or t.device != device:
-        _same(name, t, dtype, device)
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), shape))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    if t.dtype is dtype and t.device == device and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _fault(name, t, dtype, device, shape)
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _rows(name: str, t, dtype, device, shape):
     """The strides of a tensor of rows, its last axis contiguous."""
-    if t.dtype != dtype or t.device != device:
-        _same(name, t, dtype, device)
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), shape))
     s = t.stride()
-    if 1 in shape:   # the stride of an axis of one is never used
-        s = tuple(0 if n == 1 else x for n, x in zip(shape, s))
+    if t.dtype is dtype and t.device == device and t.shape == shape and s[-1] == 1 and 1 not in shape:
+        return s
+    _fault(name, t, dtype, device, shape)
+    s = tuple(0 if n == 1 else x for n, x in zip(shape, s))   # the stride of an axis of one is never used
     if s[-1] != 1 and shape[-1] > 1:
         raise ValueError("the last axis of %s must be contiguous" % name)
     return s
 
 
-def _pair(names: str, a, b, dtype, device, shape):
+def _pair(a_name: str, a, b_name: str, b, dtype, device, shape):
     """The strides of keys and values, which share them."""
-    s = _rows(names[:names.index(" ")], a, dtype, device, shape)
-    if _rows(names[names.rindex(" ") + 1:], b, dtype, device, shape) != s:
-        raise ValueError("%s must have the same strides" % names)
+    s = _rows(a_name, a, dtype, device, shape)
+    if b.dtype is dtype and b.device == device and b.shape == shape and b.stride() == s:
+        return s
+    if _rows(b_name, b, dtype, device, shape) != s:
+        raise ValueError("%s and %s must have the same strides" % (a_name, b_name))
     return s
 
 
@@ -88,7 +89,7 @@ def _code(name: str, t, table) -> int:
 
 def _here(device, stream) -> bool:
     """Whether a call can go ahead on the current device's current stream."""
-    return stream is None and device.index == torch.cuda.current_device()
+    return stream is None and device.index == _device()
 
 
 def _there(device, stream):
@@ -97,10 +98,11 @@ def _there(device, stream):
     return torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
 
 
-# The current stream's handle without the Stream object around it (0.1 of
-# the 2 us that torch.cuda.current_stream takes, of some 10 for a call).
-_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
+# The current device and its current stream's handle without the objects and
+# checks around them (0.2 of the 2 us that torch.cuda.current_stream takes, of
+# some 10 for a call).
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def prefix_attention(q, prefix_k, prefix_v, k, v, lengths, *, block_table=None, scale: Optional[float] = None,
@@ -128,13 +130,13 @@ def prefix_attention(q, prefix_k, prefix_v, k, v, lengths, *, block_table=None, 
     shape = B, T, Hq, D = q.shape
     P, Hkv, _ = prefix_k.shape
     sq = _rows("q", q, dtype, device, shape)
-    sp = _pair("prefix_k and prefix_v", prefix_k, prefix_v, dtype, device, (P, Hkv, D))
+    sp = _pair("prefix_k", prefix_k, "prefix_v", prefix_v, dtype, device, (P, Hkv, D))
     if block_table is None:
         S, page, pages, table, st = k.shape[1], 0, 0, 0, 0
-        sk = _pair("k and v", k, v, dtype, device, (B, S, Hkv, D))
+        sk = _pair("k", k, "v", v, dtype, device, (B, S, Hkv, D))
     else:
         pages, page = k.shape[:2]
-        sk = _pair("k and v", k, v, dtype, device, (pages, page, Hkv, D))
+        sk = _pair("k", k, "v", v, dtype, device, (pages, page, Hkv, D))
         if block_table.dim() != 2:
             raise ValueError("block_table must be [B, pages]")
         st = block_table.shape[1]
@@ -142,7 +144,7 @@ def prefix_attention(q, prefix_k, prefix_v, k, v, lengths, *, block_table=None, 
         S = st * page
     n = _flat("lengths", lengths, torch.int32, device, (B,))
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
+        out = q.new_empty(shape)
         o = out.data_ptr()
     else:
         o = _flat("out", out, dtype, device, shape)
@@ -153,7 +155,7 @@ def prefix_attention(q, prefix_k, prefix_v, k, v, lengths, *, block_table=None, 
         sp[0], sp[1], sk[0], sk[1], sk[2], st, D ** -0.5 if scale is None else scale)
     L = lib()
     nbytes = L.df11_prefix_attention_workspace_bytes(args)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws = lengths.new_empty((nbytes + 3) // 4)
     rc = L.df11_prefix_attention(args, ws.data_ptr(), nbytes, _stream(device.index))
     if rc:
         check(rc, "df11_prefix_attention")
@@ -174,9 +176,9 @@ class BoundedCache:
         self.code = _code("k", k, _DTYPES)
         if k.dim() != 4:
             raise ValueError("k must be [B, Hkv, slots, D]")
-        shape = B, H, C, D = tuple(k.shape)
+        shape = B, H, C, D = k.shape
         dtype, device = k.dtype, k.device
-        s = _pair("k and v", k, v, dtype, device, shape)
+        s = _pair("k", k, "v", v, dtype, device, shape)
         self.k, self.v, self.weights, self.positions, self.lengths = k, v, weights, positions, lengths
         self.shape, self.dtype, self.device = shape, dtype, device
         self.args = _CACHE.pack(k.data_ptr(), v.data_ptr(),
@@ -212,18 +214,18 @@ def cache_attention(q, cache: BoundedCache, pos, *, scale: Optional[float] = Non
         raise ValueError("q must be [B, T, Hq, D]")
     shape = B, T, Hq, D = q.shape
     if B != cache.shape[0] or D != cache.shape[3]:
-        raise ValueError("q has shape %s, the cache %s" % (tuple(shape), cache.shape))
+        raise ValueError("q has shape %s, the cache %s" % (tuple(shape), tuple(cache.shape)))
     sq = _rows("q", q, dtype, device, shape)
     p = _flat("pos", pos, torch.int32, device, (B,))
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
+        out = q.new_empty(shape)
         o = out.data_ptr()
     else:
         o = _flat("out", out, dtype, device, shape)
     args = _CACHE_ARGS.pack(q.data_ptr(), p, o, T, Hq, sq[0], sq[1], sq[2], D ** -0.5 if scale is None else scale)
     L = lib()
     nbytes = L.df11_cache_attention_workspace_bytes(cache.args, args)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws = pos.new_empty((nbytes + 3) // 4)
     rc = L.df11_cache_attention(cache.args, args, ws.data_ptr(), nbytes, _stream(device.index))
     if rc:
         check(rc, "df11_cache_attention")
@@ -243,10 +245,10 @@ def cache_insert(cache: BoundedCache, k_new, v_new, pos, recent: int, *, stream=
         with _there(device, stream):
             return cache_insert(cache, k_new, v_new, pos, recent)
     B, H, C, D = cache.shape
-    s = _pair("k_new and v_new", k_new, v_new, dtype, device, (B, H, D))
+    s = _pair("k_new", k_new, "v_new", v_new, dtype, device, (B, H, D))
     p = _flat("pos", pos, torch.int32, device, (B,))
-    slots = torch.empty((B, H), dtype=torch.int32, device=device)
-    lengths = torch.empty((B,), dtype=torch.int32, device=device)
+    slots = pos.new_empty((B, H))
+    lengths = torch.empty_like(pos)
     rc = lib().df11_cache_insert(cache.args, k_new.data_ptr(), v_new.data_ptr(), s[0], s[1], p, recent, slots.data_ptr(),
                                  lengths.data_ptr(), _stream(device.index))
     if rc:
@@ -269,10 +271,10 @@ def cache_compact(cache: BoundedCache, pos, budget: int, recent: int, *, slots: 
     if slots < 1:
         raise ValueError("the new cache needs a slot")
     p = _flat("pos", pos, torch.int32, device, (B,))
-    k = torch.empty((B, H, slots, D), dtype=dtype, device=device)
-    kept = torch.empty((B, H, slots), dtype=torch.int32, device=device)
-    cut = BoundedCache(k, torch.empty_like(k), torch.empty((B, H, slots), dtype=torch.float32, device=device),
-                       torch.empty_like(kept), torch.empty_like(cache.lengths))
+    k = cache.k.new_empty((B, H, slots, D))
+    kept = pos.new_empty((B, H, slots))
+    cut = BoundedCache(k, torch.empty_like(k), cache.weights.new_empty((B, H, slots)), torch.empty_like(kept),
+                       torch.empty_like(pos))
     rc = lib().df11_cache_compact(cache.args, p, budget, recent, cut.args, kept.data_ptr(), cut.lengths.data_ptr(),
                                   _stream(device.index))
     if rc:
@@ -310,13 +312,13 @@ def verify_drafts(draft_tokens, target_probs, uniforms, draft_probs=None, *, cou
         sq, q = _rows("draft_probs", draft_probs, dtype, device, (B, G, V)), draft_probs.data_ptr()
     u = _flat("uniforms", uniforms, torch.float32, device, (B, G + 1))
     n = 0 if counts is None else _flat("counts", counts, torch.int32, device, (B,))
-    tokens = torch.empty((B, G + 1), dtype=kind, device=device)
+    tokens = draft_tokens.new_empty((B, G + 1))
     accepted = torch.empty((B,), dtype=torch.int32, device=device)
     args = _VERIFY_ARGS.pack(d, n, target_probs.data_ptr(), q, u, tokens.data_ptr(), accepted.data_ptr(), code,
                              kind.itemsize, B, G, V, sp[0], sp[1], sq[0], sq[1])
     L = lib()
     nbytes = L.df11_verify_drafts_workspace_bytes(args)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    ws = accepted.new_empty(nbytes // 4) if nbytes else None
     rc = L.df11_verify_drafts(args, ws.data_ptr() if nbytes else 0, nbytes, _stream(device.index))
     if rc:
         check(rc, "df11_verify_drafts")
