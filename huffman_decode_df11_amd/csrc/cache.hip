@@ -84,31 +84,57 @@ __device__ __forceinline__ uint32_t worth(int32_t at, float w, int32_t pos, int6
     return at >= pos || at < 0 ? 0 : max(late, max(1u, order_of(w)));
 }
 
+constexpr int kBins = 4096;
+
+// From the greatest bin down: the one in which `left` is reached, and what is
+// in those above it (every thread gets both; there is one).
+__device__ __forceinline__ void pick(const uint32_t *bins, int each, uint32_t left, uint32_t *part, uint32_t *picked,
+                                     uint32_t &bin, uint32_t &above)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, top = each * kSelectThreads - 1 - each * (int)threadIdx.x;
+    uint32_t sum = 0;
+    for (int i = 0; i < each; i++) sum += bins[top - i];
+    uint32_t s = sum;
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t y = __shfl_up(s, d);
+        if (lane >= d) s += y;
+    }
+    if (lane == 63) part[wave] = s;
+    __syncthreads();
+    s -= sum;
+    for (int w = 0; w < kSelectWaves; w++) s += w < wave ? part[w] : 0;
+    if (s < left && left <= s + sum) {
+        int i = 0;
+        while (s + bins[top - i] < left) s += bins[top - i++];
+        picked[0] = top - i, picked[1] = s;
+    }
+    __syncthreads();
+    bin = picked[0], above = picked[1];
+}
+
 // One workgroup for each sequence and key head.  A wave holds the worths of
-// 64 * N slots in a row, N to a lane, in registers; the worth of the last
-// slot that stays is found two bits at a time by counting (a comparison's
-// mask and its population count: no histogram, whose few busy bins would
-// serialise), then each wave writes its kept slots behind those of the waves
-// before it.  A cache of more than 1024 N slots is taken in rounds, whose
-// worths are computed again for each count.
+// 64 * N slots in a row, N to a lane, in registers.  The worth of the last
+// slot that stays is found from its 12 top bits down to its 10 lowest by
+// counting the slots that share the bits found so far in bins (the recent
+// window and slots worth nothing, each of one worth, are not counted there);
+// then each wave writes its kept slots' indexes behind those of the waves
+// before it.  What the slots hold is moved by move_kernel: here that would
+// wait for memory once for each of a lane's N.  A cache of more than 1024 N
+// slots is taken in rounds, whose worths are computed again for each pass.
 template <int N>
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const Cache c, const int32_t *pos, int32_t budget,
-                                                                int64_t recent, const Cache out, int32_t *kept,
+                                                                int64_t recent, int32_t out_slots, int32_t *kept,
                                                                 int32_t *out_lengths)
 {
     constexpr int kRound = kSelectThreads * N;
-    __shared__ uint32_t counts[16][3];
+    __shared__ uint32_t bins[kBins], part[kSelectWaves], picked[2], total[2];
     __shared__ uint32_t waves[2][kSelectWaves][2];
-    __shared__ uint32_t above;
     const int bh = blockIdx.x, b = bh / c.kv_heads, lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = max(0, min(c.lengths[b], c.slots)), p = pos[b];
-    const int64_t row = (int64_t)bh * c.slots, out_row = (int64_t)bh * out.slots;
+    const int64_t row = (int64_t)bh * c.slots, out_row = (int64_t)bh * out_slots;
     const int rounds = (n + kRound - 1) / kRound;
     if (threadIdx.x == 0 && bh % c.kv_heads == 0) out_lengths[b] = min(n, budget);
-    if (threadIdx.x < 48) counts[threadIdx.x / 3][threadIdx.x % 3] = 0;
-    if (threadIdx.x == 0) above = 0;
-    __syncthreads();
 
     uint32_t w[N];
     const auto load = [&](int round) {
@@ -125,39 +151,42 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const Cache c, c
     };
     if (rounds == 1) load(0);
 
-    // the greatest worth that at least `budget` slots reach
-    uint32_t limit = 0;
-    for (int pass = 0; pass < 16; pass++) {
-        const uint32_t bit = 1u << (30 - 2 * pass);
-        uint32_t many[3] = {0, 0, 0};
+    uint32_t limit = 0, above = 0, left = budget;   // slots worth more than `limit`, and what is left to take of the others
+    bool sought = true;
+    for (int pass = 0; pass < 3 && sought; pass++) {
+        const int low = pass == 0 ? 20 : pass == 1 ? 10 : 0, high = pass == 0 ? 32 : low + 10;
+        for (int i = threadIdx.x; i < kBins; i += kSelectThreads) bins[i] = 0;
+        if (pass == 0 && threadIdx.x < 2) total[threadIdx.x] = 0;
+        __syncthreads();
+        uint32_t late = 0, others = 0;
         for (int round = 0; round < rounds; round++) {
             if (rounds > 1) load(round);
 #pragma unroll
-            for (int j = 0; j < N; j++)
-#pragma unroll
-                for (int k = 0; k < 3; k++) many[k] += __popcll(__ballot(w[j] >= limit + (k + 1) * bit));
+            for (int j = 0; j < N; j++) {
+                const bool counts = w[j] - 1u < 0xfffffffeu;
+                if (pass == 0) {
+                    late += __popcll(__ballot(w[j] == 0xffffffffu));
+                    others += __popcll(__ballot(counts));
+                }
+                if (counts && (pass == 0 || w[j] >> high == limit >> high)) atomicAdd(&bins[w[j] >> low & ((1u << (high - low)) - 1)], 1u);
+            }
         }
-        if (lane == 0)
-#pragma unroll
-            for (int k = 0; k < 3; k++) atomicAdd(&counts[pass][k], many[k]);
+        if (pass == 0 && lane == 0) atomicAdd(&total[0], late), atomicAdd(&total[1], others);
         __syncthreads();
-        uint32_t up = 0;
-#pragma unroll
-        for (int k = 0; k < 3; k++) up += counts[pass][k] >= (uint32_t)budget;
-        limit += up * bit;
+        if (pass == 0) {
+            late = total[0], others = total[1];
+            if (late >= left) limit = 0xffffffffu, sought = false;       // the window alone
+            else if (others <= left - late) above = late + others, left = 0, sought = false;   // all that is worth anything
+            else above = late, left -= late;
+            if (!sought) break;
+        }
+        uint32_t bin, over;
+        pick(bins, pass == 0 ? kBins / kSelectThreads : 1, left, part, picked, bin, over);
+        limit |= bin << low, above += over, left -= over;
+        __syncthreads();
     }
-    if (limit == 0) limit = 1;   // fewer than `budget` slots are worth anything: all of those
-
-    uint32_t g = 0;
-    for (int round = 0; round < rounds; round++) {
-        if (rounds > 1) load(round);
-#pragma unroll
-        for (int j = 0; j < N; j++) g += __popcll(__ballot(w[j] > limit));
-    }
-    if (lane == 0) atomicAdd(&above, g);
-    __syncthreads();
-    // of the slots worth just `limit` the first `want` stay
-    const uint32_t want = budget - above;
+    // of the slots worth just `limit` the first `want` stay, but none that is worth nothing
+    const uint32_t want = limit ? budget - above : 0;
     const uint64_t before = (1ull << lane) - 1;
     uint32_t more = 0, equal = 0;   // slots worth more and just `limit` in the rounds so far
     for (int round = 0; round < rounds; round++) {
@@ -183,31 +212,30 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const Cache c, c
             const uint32_t rank = e + __popcll(same & before);
             if (w[j] > limit || (w[j] == limit && rank < want)) {
                 const int i = round * kRound + (wave * N + j) * 64 + lane;
-                const int64_t to = out_row + m + __popcll(over & before) + min(rank, want);
-                kept[to] = i;
-                out.weights[to] = c.weights[row + i];
-                out.positions[to] = c.positions[row + i];
+                kept[out_row + m + __popcll(over & before) + min(rank, want)] = i;
             }
             m += __popcll(over), e += __popcll(same);
         }
     }
     const int done = more + min(equal, want);
-    for (int i = done + threadIdx.x; i < out.slots; i += kSelectThreads) {
-        kept[out_row + i] = -1;
-        out.weights[out_row + i] = 0.0f;
-        out.positions[out_row + i] = DF11_NO_TOKEN;
-    }
+    for (int i = done + threadIdx.x; i < out_slots; i += kSelectThreads) kept[out_row + i] = -1;
 }
 
-// A quarter of a wave copies (or clears) one slot's key and value.
+// A quarter of a wave moves (or clears) one slot.
 __global__ void __launch_bounds__(256) move_kernel(const Cache c, const Cache out, const int32_t *kept)
 {
     const int bh = blockIdx.y, b = bh / c.kv_heads, head = bh % c.kv_heads;
     const int i = blockIdx.x * 16 + threadIdx.x / 16;
     if (i >= out.slots) return;
-    const int from = kept[(int64_t)bh * out.slots + i];
+    const int64_t to = (int64_t)bh * out.slots + i;
+    const int from = kept[to];
     const int64_t src = b * c.stride_batch + head * c.stride_head + (int64_t)max(from, 0) * c.stride_slot;
     const int64_t dst = b * out.stride_batch + head * out.stride_head + (int64_t)i * out.stride_slot;
+    if ((threadIdx.x & 15) == 0) {
+        const int64_t at = (int64_t)bh * c.slots + max(from, 0);
+        out.weights[to] = from < 0 ? 0.0f : c.weights[at];
+        out.positions[to] = from < 0 ? DF11_NO_TOKEN : c.positions[at];
+    }
     for (int d = 8 * (threadIdx.x & 15); d < c.dim; d += 128) {
         const u32x4 zero{0, 0, 0, 0};
         const u32x4 k = from < 0 ? zero : *(const u32x4 *)(c.k + src + d);
@@ -288,9 +316,11 @@ extern "C" int df11_cache_compact(const df11_cache *cache, const int32_t *pos, i
     hipStream_t st = (hipStream_t)stream;
     const dim3 heads(c.batch * c.kv_heads), threads(kSelectThreads);
     if (c.slots <= 8 * kSelectThreads)
-        hipLaunchKernelGGL(select_kernel<8>, heads, threads, 0, st, c, pos, (int32_t)budget, recent, out, kept, out_lengths);
+        hipLaunchKernelGGL(select_kernel<8>, heads, threads, 0, st, c, pos, (int32_t)budget, recent, out.slots,
+                           kept, out_lengths);
     else
-        hipLaunchKernelGGL(select_kernel<32>, heads, threads, 0, st, c, pos, (int32_t)budget, recent, out, kept, out_lengths);
+        hipLaunchKernelGGL(select_kernel<32>, heads, threads, 0, st, c, pos, (int32_t)budget, recent, out.slots,
+                           kept, out_lengths);
     hipLaunchKernelGGL(move_kernel, dim3((out.slots + 15) / 16, c.batch * c.kv_heads), dim3(256), 0, st, c, out, kept);
     return launched(who);
 }
