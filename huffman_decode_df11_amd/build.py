@@ -3,6 +3,7 @@
     python -m huffman_decode_df11_amd.build
 
 The library lands in huffman_decode_df11_amd/_build/libdf11.so, next to
+_df11_serve.so, the generation operators' Python binding (serve.py),
 df11_c_api_check, a host program that uses the C ABI alone (no Python), and
 df11_segment_bounds_check, a host program that checks the decode kernels'
 per-segment address arithmetic (segment_plan.h) on random and corrupt
@@ -29,6 +30,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libdf11.so")
+SERVE_BINDING = os.path.join(OUT_DIR, "_df11_serve.so")
 C_API_CHECK = os.path.join(OUT_DIR, "df11_c_api_check")
 BOUNDS_CHECK = os.path.join(OUT_DIR, "df11_segment_bounds_check")
 SAN_DIR = os.path.join(PKG, "_build_san")
@@ -76,10 +78,13 @@ def build(verbose: bool = False) -> str:
         obj = os.path.join(OUT_DIR, src + ".o")
         cmds.append(["g++", *CXX_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj])
         objs.append(obj)
+    binding = SERVE_BINDING + ".tmp%d" % os.getpid()
+    cmds.append(serve_binding_command(binding))
     if verbose:
         for c in cmds:
             print(" ".join(c))
     _run_all(cmds)
+    os.replace(binding, SERVE_BINDING)
     tmp = LIB + ".tmp%d" % os.getpid()
     _run_all([[HIPCC, "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", tmp, *objs]])
     os.replace(tmp, LIB)
@@ -94,6 +99,20 @@ def build(verbose: bool = False) -> str:
                "-o", tmp]])
     os.replace(tmp, BOUNDS_CHECK)
     return LIB
+
+
+def serve_binding_command(out: str):
+    """The compiler line of the generation operators' Python binding
+    (csrc/serve_bind.cpp), against the torch of this interpreter."""
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    include = [d for d in cpp_extension.include_paths()] + [sysconfig.get_paths()["include"]]
+    libdir = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+            *sum((["-isystem", d] for d in include), []), "-I", INCLUDE, os.path.join(CSRC, "serve_bind.cpp"),
+            "-L", libdir, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-o", out]
 
 
 SAN_FLAGS = ["-fsanitize=address", "-fsanitize=undefined", "-fno-sanitize-recover=undefined",
