@@ -78,6 +78,32 @@ class GemmTuning(ctypes.Structure):
                 ("tiles_per_wave", u32), ("k_slices", u32), ("reserved", u32)]
 
 
+def _fields(pointers: str, numbers: str, reals: str = ""):
+    """Fields of 8 bytes each: addresses, whole numbers, reals."""
+    return ([(n, ctypes.c_void_p) for n in pointers.split()] + [(n, i64) for n in numbers.split()] +
+            [(n, ctypes.c_double) for n in reals.split()])
+
+
+class PrefixAttentionArgs(ctypes.Structure):
+    _fields_ = _fields("q prefix_k prefix_v k v lengths block_table out lse",
+                       "dtype batch tokens heads kv_heads dim prefix suffix page n_pages q_batch q_token q_head "
+                       "prefix_token prefix_head k_batch k_token k_head table_batch", "scale")
+
+
+class Cache(ctypes.Structure):
+    _fields_ = _fields("k v weights positions lengths",
+                       "dtype batch kv_heads slots dim stride_batch stride_head stride_slot")
+
+
+class CacheAttentionArgs(ctypes.Structure):
+    _fields_ = _fields("q pos out", "tokens heads q_batch q_token q_head", "scale")
+
+
+class VerifyArgs(ctypes.Structure):
+    _fields_ = _fields("draft_tokens counts target_probs draft_probs uniforms tokens accepted",
+                       "dtype token_bytes batch drafts vocab target_batch target_row draft_batch draft_row")
+
+
 # (field, element ctype) of every array in a view
 VIEW_ARRAYS = (
     ("exp_words", ctypes.c_uint32),
@@ -155,15 +181,16 @@ def lib():
     L.df11_device_encoded_free.restype = None
     L.df11_device_encoded_view.argtypes = [vp, ctypes.POINTER(View)]
     L.df11_device_encoded_to_host.argtypes = [vp, ctypes.POINTER(vp)]
-    # argument structs of the generation operators arrive packed (serve.py)
-    L.df11_prefix_attention_workspace_bytes.argtypes = [vp]
-    L.df11_prefix_attention.argtypes = [vp, vp, u64, vp]
-    L.df11_cache_attention_workspace_bytes.argtypes = [vp, vp]
-    L.df11_cache_attention.argtypes = [vp, vp, vp, u64, vp]
-    L.df11_cache_insert.argtypes = [vp, vp, vp, i64, i64, vp, i64, vp, vp, vp]
-    L.df11_cache_compact.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp]
-    L.df11_verify_drafts_workspace_bytes.argtypes = [vp]
-    L.df11_verify_drafts.argtypes = [vp, vp, u64, vp]
+    prefix, cache, verify = (ctypes.POINTER(s) for s in (PrefixAttentionArgs, Cache, VerifyArgs))
+    attend = ctypes.POINTER(CacheAttentionArgs)
+    L.df11_prefix_attention_workspace_bytes.argtypes = [prefix]
+    L.df11_prefix_attention.argtypes = [prefix, vp, u64, vp]
+    L.df11_cache_attention_workspace_bytes.argtypes = [cache, attend]
+    L.df11_cache_attention.argtypes = [cache, attend, vp, u64, vp]
+    L.df11_cache_insert.argtypes = [cache, vp, vp, i64, i64, vp, i64, vp, vp, vp]
+    L.df11_cache_compact.argtypes = [cache, vp, i64, i64, cache, vp, vp, vp]
+    L.df11_verify_drafts_workspace_bytes.argtypes = [verify]
+    L.df11_verify_drafts.argtypes = [verify, vp, u64, vp]
     for name in ("df11_prefix_attention_workspace_bytes", "df11_cache_attention_workspace_bytes",
                  "df11_verify_drafts_workspace_bytes"):
         getattr(L, name).restype = u64

@@ -580,6 +580,8 @@ def test_refusals():
         serve.BoundedCache(cache.k, cache.v, cache.weights.half(), cache.positions, cache.lengths)
     with pytest.raises(ValueError):
         serve.BoundedCache(cache.k, cache.v, cache.weights[:1], cache.positions, cache.lengths)
+    with pytest.raises(AttributeError):
+        cache.lengths = n
     with pytest.raises(ValueError):
         serve.cache_attention(z(3, 1, 4, 64, dtype=BF, device="cuda"), cache, n)
     with pytest.raises(ValueError):
