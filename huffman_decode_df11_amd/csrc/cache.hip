@@ -24,7 +24,8 @@ struct Cache {
     int64_t stride_batch, stride_head, stride_slot;
 };
 
-constexpr int kInsertThreads = 256;
+constexpr int kInsertThreads = 512;
+constexpr int kInsertEach = 8;   // slots a thread reads at a time
 
 // One workgroup for each sequence and key head.  A slot's rank is one 64-bit
 // number, its kind (0 stale, 1 outside the recent window, 2 neither) above
@@ -43,16 +44,30 @@ __global__ void __launch_bounds__(kInsertThreads) insert_kernel(const Cache c, c
         return;
     }
     const int64_t row = (int64_t)bh * c.slots;
+    // the new row, on its way while its slot is looked for (dim / 8 threads, at most 32)
+    const int64_t from = b * new_batch + head * new_head;
+    const int d = 8 * threadIdx.x;
+    u32x4 key{0, 0, 0, 0}, value{0, 0, 0, 0};
+    if (d < c.dim) key = *(const u32x4 *)(k_new + from + d), value = *(const u32x4 *)(v_new + from + d);
     int slot = n;
     if (n == c.slots) {
         uint64_t best = ~0ull;
-#pragma unroll 8
-        for (int i = threadIdx.x; i < n; i += kInsertThreads) {
-            const int32_t at = c.positions[row + i];
-            const float w = c.weights[row + i];   // read with the position, not behind it
-            const uint64_t kind = at >= p || at < 0 ? 0 : (int64_t)at <= (int64_t)p - recent ? 1 : 2;
-            const uint32_t value = kind == 0 ? 0 : kind == 1 ? order_of(w) : (uint32_t)at ^ 0x80000000u;
-            best = min(best, kind << 62 | (uint64_t)value << 30 | (uint32_t)i);
+        for (int i0 = threadIdx.x; i0 < n; i0 += kInsertEach * kInsertThreads) {
+            int32_t places[kInsertEach];
+            float weights[kInsertEach];
+#pragma unroll
+            for (int j = 0; j < kInsertEach; j++) {
+                const int64_t i = row + min(i0 + j * kInsertThreads, n - 1);
+                places[j] = c.positions[i], weights[j] = c.weights[i];
+            }
+#pragma unroll
+            for (int j = 0; j < kInsertEach; j++) {
+                const int i = min(i0 + j * kInsertThreads, n - 1);   // the last slot again does not change the least
+                const int32_t at = places[j];
+                const uint64_t kind = at >= p || at < 0 ? 0 : (int64_t)at <= (int64_t)p - recent ? 1 : 2;
+                const uint32_t order = kind == 0 ? 0 : kind == 1 ? order_of(weights[j]) : (uint32_t)at ^ 0x80000000u;
+                best = min(best, kind << 62 | (uint64_t)order << 30 | (uint32_t)i);
+            }
         }
         for (int d = 32; d; d >>= 1) best = min(best, (uint64_t)__shfl_xor((unsigned long long)best, d));
         if ((threadIdx.x & 63) == 0) least[threadIdx.x >> 6] = best;
@@ -61,11 +76,7 @@ __global__ void __launch_bounds__(kInsertThreads) insert_kernel(const Cache c, c
         slot = (int)(best & 0x3fffffff);
     }
     const int64_t to = b * c.stride_batch + head * c.stride_head + slot * c.stride_slot;
-    const int64_t from = b * new_batch + head * new_head;
-    for (int d = 8 * threadIdx.x; d < c.dim; d += 8 * kInsertThreads) {
-        *(u32x4 *)(c.k + to + d) = *(const u32x4 *)(k_new + from + d);
-        *(u32x4 *)(c.v + to + d) = *(const u32x4 *)(v_new + from + d);
-    }
+    if (d < c.dim) *(u32x4 *)(c.k + to + d) = key, *(u32x4 *)(c.v + to + d) = value;
     if (threadIdx.x == 0) {
         c.weights[row + slot] = 0.0f;
         c.positions[row + slot] = p;

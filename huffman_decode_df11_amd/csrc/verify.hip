@@ -31,9 +31,10 @@ struct Args {
     int32_t *taken;  // [batch]
 };
 
-constexpr int kThreads = 256;
-constexpr int kRun = 32;                         // tokens a thread holds in the last search
-constexpr int kPiece = kThreads * kRun;          // tokens of a part: 2^13, so that a part's sum is below 2^53
+constexpr int kPiece = 8192;            // tokens of a part: a thread's sum of up to 2^40 each is below 2^53
+constexpr int kPartThreads = 256;       // of a part's sums: 32 tokens a thread
+constexpr int kDrawThreads = 1024;      // of a sequence's draw, which is all latency: 8 tokens a thread
+constexpr int kRun = kPiece / kDrawThreads;
 
 struct F32 {
     typedef float type;
@@ -72,20 +73,14 @@ __device__ __forceinline__ u64 wave_sum(u64 x)
     return x;
 }
 
-// Sum over the workgroup of the values before this thread's.
-__device__ __forceinline__ u64 sum_before(u64 x, u64 *part)
+// Sums over the wave of the values up to this lane's.
+__device__ __forceinline__ u64 wave_scan(u64 s)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    u64 s = x;
+    const int lane = threadIdx.x & 63;
     for (int d = 1; d < 64; d <<= 1) {
         const u64 y = __shfl_up(s, d);
         if (lane >= d) s += y;
     }
-    __syncthreads();
-    if (lane == 63) part[wave] = s;
-    __syncthreads();
-    s -= x;
-    for (int w = 0; w < wave; w++) s += part[w];
     return s;
 }
 
@@ -102,7 +97,7 @@ struct Rows {
 };
 
 // The number of drafts taken: where the first is refused.
-template <class T>
+template <class T, int kThreads>
 __device__ __forceinline__ int drafts_taken(const Args &a, int b, int count, int *lds)
 {
     typedef typename T::type type;
@@ -135,7 +130,7 @@ __device__ __forceinline__ Rows<T> rows_of(const Args &a, int b, int count, int 
 // The sums over tokens [i0, i1) of max(p - q, 0) (of p behind the last
 // draft) and of p, complete in thread 0.  16 bytes of a row a thread at a
 // time, at any alignment.
-template <class T>
+template <class T, int kThreads>
 __device__ __forceinline__ void part_sums(const Rows<T> &r, int i0, int i1, u64 *lds, u64 &rest, u64 &all)
 {
     typedef typename T::type type;
@@ -174,16 +169,16 @@ __device__ __forceinline__ void part_sums(const Rows<T> &r, int i0, int i1, u64 
 
 // Parts of the vocabulary: each writes its two sums.
 template <class T>
-__global__ void __launch_bounds__(kThreads) part_kernel(const Args a)
+__global__ void __launch_bounds__(kPartThreads) part_kernel(const Args a)
 {
-    __shared__ u64 lds[2 * kThreads / 64];
+    __shared__ u64 lds[2 * kPartThreads / 64];
     __shared__ int first_refused;
     const int part = blockIdx.x, b = blockIdx.y;
     const int count = a.counts ? max(0, min(a.counts[b], a.drafts)) : a.drafts;
-    const int n = drafts_taken<T>(a, b, count, &first_refused);
+    const int n = drafts_taken<T, kPartThreads>(a, b, count, &first_refused);
     if (part == 0 && threadIdx.x == 0) a.taken[b] = n;
     u64 rest, all;
-    part_sums<T>(rows_of<T>(a, b, count, n), part * kPiece, min(a.vocab, (part + 1) * kPiece), lds, rest, all);
+    part_sums<T, kPartThreads>(rows_of<T>(a, b, count, n), part * kPiece, min(a.vocab, (part + 1) * kPiece), lds, rest, all);
     if (threadIdx.x == 0) {
         u64 *to = a.sums + ((int64_t)b * a.parts + part) * 2;
         to[0] = rest, to[1] = all;
@@ -194,60 +189,55 @@ __global__ void __launch_bounds__(kThreads) part_kernel(const Args a)
 // whole sum, in it the thread's run, and in that the token.  A vocabulary of
 // one part is summed here too.
 template <class T>
-__global__ void __launch_bounds__(kThreads) draw_kernel(const Args a)
+__global__ void __launch_bounds__(kDrawThreads) draw_kernel(const Args a)
 {
-    __shared__ u64 lds[2 * kThreads / 64];
-    __shared__ u64 before_part;
-    __shared__ int first_refused, chosen, drawn;
-    const int b = blockIdx.x;
+    constexpr int kWaves = kDrawThreads / 64;
+    __shared__ u64 lds[2 * kWaves];
+    __shared__ int first_refused, drawn;
+    const int b = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int count = a.counts ? max(0, min(a.counts[b], a.drafts)) : a.drafts;
-    const int n = a.parts > 1 ? a.taken[b] : drafts_taken<T>(a, b, count, &first_refused);
+    if (threadIdx.x == 0) drawn = -1;
+    const int n = a.parts > 1 ? a.taken[b] : drafts_taken<T, kDrawThreads>(a, b, count, &first_refused);
     Rows<T> r = rows_of<T>(a, b, count, n);
     const float last = a.uniforms[(int64_t)b * (a.drafts + 1) + a.drafts];
     const u64 u = (u64)(fminf(fmaxf(last, 0.0f), 0.99999994f) * 16777216.0f);
     u64 rest = 0, all = 0;
-    if (threadIdx.x == 0) drawn = -1, chosen = 0, before_part = 0;
+    const u64 *sums = a.sums + (int64_t)b * a.parts * 2;
     if (a.parts == 1) {
-        part_sums<T>(r, 0, a.vocab, lds, rest, all);
+        part_sums<T, kDrawThreads>(r, 0, a.vocab, lds, rest, all);
     } else {
-        u64 mine[2] = {0, 0};
-        for (int i = threadIdx.x; i < a.parts; i += kThreads) {
-            const u64 *from = a.sums + ((int64_t)b * a.parts + i) * 2;
-            mine[0] += from[0], mine[1] += from[1];
-        }
-        mine[0] = wave_sum(mine[0]), mine[1] = wave_sum(mine[1]);
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        if (lane == 0) lds[wave] = mine[0], lds[kThreads / 64 + wave] = mine[1];
-        __syncthreads();
-        for (int w = 0; w < kThreads / 64; w++) rest += lds[w], all += lds[kThreads / 64 + w];
+        // every wave for itself: no wave waits for another
+        for (int i = lane; i < a.parts; i += 64) rest += sums[2 * i], all += sums[2 * i + 1];
+        rest = wave_sum(rest), all = wave_sum(all);
     }
     if (!rest) r.rest = false;   // nothing is left of p - q: p itself
     const u64 total = rest ? rest : all;
     const u64 goal = __umul64hi(u << 40, total);   // floor(u * total / 2^24), below total
+    int part = 0;
+    u64 before = 0;
     if (a.parts > 1) {
-        // at most 512 parts: two for each thread, in order
-        u64 x[2];
-        for (int j = 0; j < 2; j++) {
-            const int i = 2 * threadIdx.x + j;
-            x[j] = i < a.parts ? a.sums[((int64_t)b * a.parts + i) * 2 + (rest ? 0 : 1)] : 0;
-        }
-        u64 s = sum_before(x[0] + x[1], lds);
-        for (int j = 0; j < 2; j++) {
-            if (s <= goal && goal < s + x[j]) chosen = 2 * threadIdx.x + j, before_part = s;
-            s += x[j];
+        for (int i0 = 0; i0 < a.parts; i0 += 64) {
+            const u64 x = i0 + lane < a.parts ? sums[2 * (i0 + lane) + (rest ? 0 : 1)] : 0;
+            const u64 s = before + wave_scan(x);
+            const u64 past = __ballot(goal < s);
+            if (past) {
+                const int l = __builtin_ctzll(past);
+                part = i0 + l, before = __shfl(s - x, l);
+                break;
+            }
+            before = __shfl(s, 63);
         }
     }
-    __syncthreads();
     // the part, kRun tokens in a row to a thread
-    const int part = chosen, first = part * kPiece + threadIdx.x * kRun;
+    const int first = part * kPiece + threadIdx.x * kRun;
     typedef typename T::type type;
-    constexpr int V = 16 / sizeof(type);
+    constexpr int V = 16 / sizeof(type) < kRun ? 16 / sizeof(type) : kRun;
     type p[kRun], q[kRun];
 #pragma unroll
     for (int v = 0; v < kRun; v += V) {
         if (first + v + V <= a.vocab) {
-            __builtin_memcpy(p + v, r.p + first + v, 16);
-            if (r.q) __builtin_memcpy(q + v, r.q + first + v, 16);
+            __builtin_memcpy(p + v, r.p + first + v, V * sizeof(type));
+            if (r.q) __builtin_memcpy(q + v, r.q + first + v, V * sizeof(type));
         } else {
 #pragma unroll
             for (int j = 0; j < V; j++) {
@@ -257,24 +247,29 @@ __global__ void __launch_bounds__(kThreads) draw_kernel(const Args a)
             }
         }
     }
-    const auto weight = [&](int j) {
-        const double x = whole(T::value(p[j]));
-        return r.rest ? r.left(x, r.q ? whole(T::value(q[j])) : r.refused(first + j)) : x;
-    };
-    double sum = 0.0;
+    double x[kRun], sum = 0.0;
 #pragma unroll
-    for (int j = 0; j < kRun; j++) sum += weight(j);
-    u64 s = before_part + sum_before((u64)sum, lds);
-    if (s <= goal && goal < s + (u64)sum) {
+    for (int j = 0; j < kRun; j++) {
+        x[j] = whole(T::value(p[j]));
+        if (r.rest) x[j] = r.left(x[j], r.q ? whole(T::value(q[j])) : r.refused(first + j));
+        sum += x[j];
+    }
+    const u64 mine = (u64)sum;
+    u64 s = wave_scan(mine);
+    __syncthreads();
+    if (lane == 63) lds[wave] = s;
+    __syncthreads();
+    s += before - mine;
+    for (int w = 0; w < wave; w++) s += lds[w];
+    if (s <= goal && goal < s + mine) {
 #pragma unroll
         for (int j = 0; j < kRun; j++) {
-            const u64 x = (u64)weight(j);
-            if (s <= goal && goal < s + x) drawn = first + j;
-            s += x;
+            if (s <= goal && goal < s + (u64)x[j]) drawn = first + j;
+            s += (u64)x[j];
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i <= a.drafts; i += kThreads) {
+    for (int i = threadIdx.x; i <= a.drafts; i += kDrawThreads) {
         const int64_t at = (int64_t)b * (a.drafts + 1) + i;
         put(a.tokens, a.token_bytes, at,
             i < n ? token(a.draft_tokens, a.token_bytes, (int64_t)b * a.drafts + i) : i == n ? drawn : -1);
@@ -285,8 +280,8 @@ __global__ void __launch_bounds__(kThreads) draw_kernel(const Args a)
 template <class T>
 int launch(const Args &a, hipStream_t st)
 {
-    if (a.parts > 1) hipLaunchKernelGGL(part_kernel<T>, dim3(a.parts, a.batch), dim3(kThreads), 0, st, a);
-    hipLaunchKernelGGL(draw_kernel<T>, dim3(a.batch), dim3(kThreads), 0, st, a);
+    if (a.parts > 1) hipLaunchKernelGGL(part_kernel<T>, dim3(a.parts, a.batch), dim3(kPartThreads), 0, st, a);
+    hipLaunchKernelGGL(draw_kernel<T>, dim3(a.batch), dim3(kDrawThreads), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return df11::fail(DF11_E_DEVICE, "df11_verify_drafts launch: %s", hipGetErrorString(e));
     return DF11_OK;
