@@ -55,9 +55,23 @@ struct Args {
     int64_t logit_stride;
     float scale2;              // scale * log2(e)
     int32_t prefix_splits, prefix_span, prefix_tiles, suffix_splits, suffix_span, suffix_tiles;
+    int32_t prefix_places;     // workgroups of the prefix
     int64_t rows;              // batch * tokens * heads
     bool big;                  // tiles of 128 rows
 };
+
+// Workgroups i and i + 8 run on one of the eight dies, which has an L2 of its
+// own: the row tiles that read the same keys and values follow each other
+// there, and the dies get the ranges of all lengths alike (with neighbouring
+// workgroups on neighbouring ranges of one sequence, two or four ranges left
+// dies idle: 528 items of 2050 to 4099 keys 121 and 113 us, 100 so).
+__device__ __forceinline__ bool place(int i, int tiles, int pairs, int &tile, int &pair)
+{
+    tile = i / 8 % tiles;
+    pair = i % 8 + i / 8 / tiles * 8;
+    return pair < pairs;
+}
+int64_t places(int64_t tiles, int64_t pairs) { return (pairs + 7) / 8 * 8 * tiles; }
 
 // The 32 keys from `base` on: rows in memory, and which of them which query
 // tokens see.  Lane l speaks for key base + l % 32: rel is the key's place
@@ -703,36 +717,30 @@ __global__ void __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) attend_kernel(
     constexpr int kLds = KIND == kTiles ? (kTile > kJoin ? kTile : kJoin) : KIND == kCacheTiles ? kTile : kJoin;
     __shared__ alignas(1024) char lds[kLds];
     if constexpr (KIND == kCacheTiles) {
-        int item = blockIdx.x;
-        const int split = item % a.suffix_splits;
-        item /= a.suffix_splits;
-        const int tile = item % a.suffix_tiles;
-        item /= a.suffix_tiles;
-        tile_block<E, DP, true>(a, lds, item / a.kv_heads, item % a.kv_heads, tile, split);
+        int tile, pair;
+        const int own = a.batch * a.kv_heads;
+        if (!place(blockIdx.x, a.suffix_tiles, own * a.suffix_splits, tile, pair)) return;
+        tile_block<E, DP, true>(a, lds, pair % own / a.kv_heads, pair % a.kv_heads, tile, pair / own);
         return;
     }
     JoinO *const join_o = (JoinO *)lds;
     JoinMl *const join_ml = (JoinMl *)(lds + kWaves * sizeof(JoinO));
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-    const int prefix_items = a.kv_heads * a.prefix_tiles * a.prefix_splits;
-    int item = blockIdx.x, split;
-    const bool in_prefix = !CACHE && item < prefix_items;
+    int tile, pair, b = 0;
+    const bool in_prefix = !CACHE && (int)blockIdx.x < a.prefix_places;
+    if (in_prefix) {
+        if (!place(blockIdx.x, a.prefix_tiles, a.kv_heads * a.prefix_splits, tile, pair)) return;
+    } else {
+        if (!place(blockIdx.x - a.prefix_places, a.suffix_tiles, a.batch * a.kv_heads * a.suffix_splits, tile, pair)) return;
+    }
+    const int head = pair % a.kv_heads;
+    int split = pair / a.kv_heads;
+    if (!in_prefix) b = split % a.batch, split /= a.batch;
     if constexpr (KIND == kTiles) {
         if (in_prefix) {
-            split = item % a.prefix_splits, item /= a.prefix_splits;
-            tile_block<E, DP, false>(a, lds, 0, item / a.prefix_tiles, item % a.prefix_tiles, split);
+            tile_block<E, DP, false>(a, lds, 0, head, tile, split);
             return;
         }
-    }
-    int tile, head, b = 0;
-    if (in_prefix) {
-        split = item % a.prefix_splits, item /= a.prefix_splits;
-        tile = item % a.prefix_tiles, head = item / a.prefix_tiles;
-    } else {
-        item -= CACHE ? 0 : prefix_items;
-        split = item % a.suffix_splits, item /= a.suffix_splits;
-        tile = item % a.suffix_tiles, item /= a.suffix_tiles;
-        head = item % a.kv_heads, b = item / a.kv_heads;
     }
     const int row_count = (in_prefix ? a.batch : 1) * a.tokens * a.group;
     const int span = in_prefix ? a.prefix_span : a.suffix_span;
@@ -1040,15 +1048,17 @@ void set_ranges(int64_t keys, int64_t n, int32_t *splits, int32_t *span)
 }
 
 // The fewest ranges with which all items' workgroups nearly fill the `slots`
-// that are resident at a time, once or several times over: 528 items of 4099
-// keys on 768 slots 120 us in 2 ranges, 102 in 4; 512 items of 2048 keys on
-// 512 slots 100 us in 1 range, 102 in 2.
+// that are resident at a time, once or several times over; one range, which
+// has the fewest sums to join, also where it fills three quarters.  528 items
+// of 2050 to 4099 keys on 768 slots: 111 us in 1 range, 108 in 2, 100 in 4;
+// 512 items of 2048 keys on 512 slots 99 us in 1 range, 102 in 2 or 4; 384
+// items of up to 700 keys on 512 slots 29 us in 1 range, 31 in 2, 32 in 4.
 int64_t ranges_that_fill(int64_t keys, int64_t items, int64_t slots)
 {
     const int64_t most = std::min<int64_t>(ceil_div(keys, kStep * kWaves), ceil_div(8 * slots, items));
     int64_t best = 1;
     double full = 0.0;
-    for (int64_t n = 1; n <= most && full < 0.9; n++) {
+    for (int64_t n = 1; n <= most && full < (n == 2 ? 0.75 : 0.9); n++) {
         const double rounds = (double)items * n / slots, x = rounds / std::ceil(rounds);
         if (x > full) full = x, best = n;
     }
@@ -1075,6 +1085,7 @@ void plan(Args &a, bool cache)
     set_ranges(a.prefix, a.big ? (alone ? 2 : 1) * cus / prefix_items : ranges_that_fill(a.prefix, prefix_items, resident * cus),
                &a.prefix_splits, &a.prefix_span);
     const int64_t suffix_items = (int64_t)a.suffix_tiles * a.kv_heads * a.batch;
+    a.prefix_places = a.prefix_splits ? places(a.prefix_tiles, (int64_t)a.kv_heads * a.prefix_splits) : 0;
     set_ranges(a.suffix, ranges_that_fill(a.suffix, suffix_items, resident * cus), &a.suffix_splits, &a.suffix_span);
 }
 
@@ -1116,9 +1127,8 @@ int strides_ok(const char *who, std::initializer_list<int64_t> strides, std::ini
 template <class E, int DP, int KIND>
 int launch(const Args &a, hipStream_t st)
 {
-    constexpr bool CACHE = KIND == kCache || KIND == kCacheTiles;
-    const int64_t items = (CACHE ? 0 : (int64_t)a.kv_heads * a.prefix_tiles * a.prefix_splits) +
-                          (int64_t)a.batch * a.kv_heads * a.suffix_tiles * a.suffix_splits;
+    const int64_t items =
+        a.prefix_places + places(a.suffix_tiles, (int64_t)a.batch * a.kv_heads * a.suffix_splits);
     const int64_t finish =
         a.rows + (KIND == kCache ? (int64_t)a.batch * a.kv_heads * ceil_div(a.suffix, kWeighKeys) : 0);
     if (items > 0x7fffffffll || finish > 0x7fffffffll)
