@@ -55,7 +55,7 @@ struct Args {
     int64_t logit_stride;
     float scale2;              // scale * log2(e)
     int32_t prefix_splits, prefix_span, prefix_tiles, suffix_splits, suffix_span, suffix_tiles;
-    int32_t prefix_places;     // workgroups of the prefix
+    int64_t prefix_places;     // workgroups of the prefix
     int64_t rows;              // batch * tokens * heads
     bool big;                  // tiles of 128 rows
 };
@@ -727,11 +727,11 @@ __global__ void __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) attend_kernel(
     JoinMl *const join_ml = (JoinMl *)(lds + kWaves * sizeof(JoinO));
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
     int tile, pair, b = 0;
-    const bool in_prefix = !CACHE && (int)blockIdx.x < a.prefix_places;
+    const bool in_prefix = !CACHE && blockIdx.x < a.prefix_places;
     if (in_prefix) {
         if (!place(blockIdx.x, a.prefix_tiles, a.kv_heads * a.prefix_splits, tile, pair)) return;
     } else {
-        if (!place(blockIdx.x - a.prefix_places, a.suffix_tiles, a.batch * a.kv_heads * a.suffix_splits, tile, pair)) return;
+        if (!place(blockIdx.x - (int)a.prefix_places, a.suffix_tiles, a.batch * a.kv_heads * a.suffix_splits, tile, pair)) return;
     }
     const int head = pair % a.kv_heads;
     int split = pair / a.kv_heads;
