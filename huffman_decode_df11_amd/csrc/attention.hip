@@ -58,6 +58,7 @@ struct Args {
     int64_t prefix_places;     // workgroups of the prefix
     int64_t rows;              // batch * tokens * heads
     bool big;                  // tiles of 128 rows
+    bool four;                 // four output rows to a joining workgroup
 };
 
 // Workgroups i and i + 8 run on one of the eight dies, which has an L2 of its
@@ -845,6 +846,14 @@ __device__ __forceinline__ float2 join_row(const Args &a, int64_t row, int parts
     return make_float2(m, l);
 }
 
+// A row's logarithm of its sum, for the caller and for the weights.
+__device__ __forceinline__ void put_top(const Args &a, int64_t row, float m, float l)
+{
+    const float top = m + __log2f(l);
+    if (a.lse) a.lse[row] = l == 0.0f ? -INFINITY : kLn2 * top;
+    if (a.tops) a.tops[row] = l == 0.0f ? INFINITY : top;   // an empty row gives no slot anything
+}
+
 // One workgroup joins the ranges of one output row: each wave takes every
 // fourth range, each lane two dims.
 template <class E>
@@ -875,11 +884,45 @@ __device__ __forceinline__ void join_block(const Args &a, int64_t row)
         for (int w = 0; w < kWaves; w++) x += sums[w][threadIdx.x].x, y += sums[w][threadIdx.x].y;
         *(uint32_t *)(a.out + row * a.dim + 2 * threadIdx.x) = E::pack(x * inv, y * inv);
     }
-    if (threadIdx.x == 0) {
-        const float top = ml.x + __log2f(ml.y);
-        if (a.lse) a.lse[row] = ml.y == 0.0f ? -INFINITY : kLn2 * top;
-        if (a.tops) a.tops[row] = ml.y == 0.0f ? INFINITY : top;   // an empty row gives no slot anything
+    if (threadIdx.x == 0) put_top(a, row, ml.x, ml.y);
+}
+
+// One wave joins the ranges (at most 64) of one output row, lane l the
+// factor of range l.  For many rows: their workgroups of four rows are
+// resident at once, where those of one row each took two rounds (4096 rows of
+// 9 ranges: 11 us).
+template <class E>
+__device__ __forceinline__ void join_wave(const Args &a, int64_t row)
+{
+    const int lane = threadIdx.x & 63;
+    const int parts = a.prefix_splits + own_splits(a, (int)(row / ((int64_t)a.tokens * a.heads)));
+    const float2 mine = lane < parts ? a.part_ml[lane * a.rows + row] : make_float2(-INFINITY, 0.0f);
+    float m = mine.x;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+    const float safe = m == -INFINITY ? 0.0f : m;
+    const float factor = exp2_fast(mine.x - safe);
+    float l = factor * mine.y;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    for (int d = 2 * lane; d < a.dim; d += 128) {
+        float x = 0.0f, y = 0.0f;
+        for (int s0 = 0; s0 < parts; s0 += 8) {
+            float2 o[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                o[j] = *(const float2 *)(a.part_o + (min(s0 + j, parts - 1) * a.rows + row) * a.dim + d);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                if (s0 + j >= parts) break;
+                const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, factor), s0 + j));
+                x += f * o[j].x, y += f * o[j].y;
+            }
+        }
+        *(uint32_t *)(a.out + row * a.dim + d) = E::pack(x * inv, y * inv);
     }
+    if (lane == 0) put_top(a, row, m, l);
 }
 
 constexpr int kWeighKeys = 1024;   // slots of a workgroup, four to a thread
@@ -1023,16 +1066,20 @@ __global__ void __launch_bounds__(64 * kWaves, 2) weigh_kernel(const Args a)
     }
 }
 
-// Workgroups below the number of output rows join one row each; behind them
-// those of bounded caches add up the slots' weights.
+// Workgroups below the number of those that join join a row each (a.four:
+// four rows); behind them those of bounded caches add up the slots' weights.
 template <class E, bool WEIGH>
 __global__ void __launch_bounds__(64 * kWaves) finish_kernel(const Args a)
 {
-    if (!WEIGH || blockIdx.x < a.rows) {
-        join_block<E>(a, blockIdx.x);
-    } else {
-        const int runs = (a.suffix + kWeighKeys - 1) / kWeighKeys, item = blockIdx.x - (int)a.rows;
+    const int64_t joins = a.four ? (a.rows + kWaves - 1) / kWaves : a.rows;
+    if (WEIGH && blockIdx.x >= joins) {
+        const int runs = (a.suffix + kWeighKeys - 1) / kWeighKeys, item = blockIdx.x - (int)joins;
         weigh_block(a, item / runs, item % runs * kWeighKeys);
+    } else if (a.four) {
+        const int64_t row = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+        if (row < a.rows) join_wave<E>(a, row);
+    } else {
+        join_block<E>(a, blockIdx.x);
     }
 }
 
@@ -1072,7 +1119,11 @@ void plan(Args &a, bool cache)
     a.rows = (int64_t)a.batch * a.tokens * a.heads;
     if (!a.rows) return;
     const int64_t own_rows = (int64_t)a.tokens * a.group, shared_rows = a.batch * own_rows;
-    a.big = (cache ? own_rows : shared_rows) > 32;
+    // 128-row tiles from where their time, nearly the same for any number of
+    // rows, is the less (us in 16- / 128-row tiles: 8191 shared positions 15.4
+    // / 17.8 at 16 rows, 19.1 / 17.3 at 24, 23.4 / 18.7 at 64; caches of 16384
+    // slots 99 / 117 at 32 rows, 135 / 120 at 48, 167 / 121 at 64).
+    a.big = cache ? own_rows > 32 : shared_rows > 16;
     a.prefix_tiles = ceil_div(shared_rows, a.big ? kTileRows : kRows);
     a.suffix_tiles = ceil_div(own_rows, cache && a.big ? kTileRows : kRows);
     // 128-row tiles: one workgroup on each CU, whose partial sums are few and
@@ -1087,6 +1138,11 @@ void plan(Args &a, bool cache)
     const int64_t suffix_items = (int64_t)a.suffix_tiles * a.kv_heads * a.batch;
     a.prefix_places = a.prefix_splits ? places(a.prefix_tiles, (int64_t)a.kv_heads * a.prefix_splits) : 0;
     set_ranges(a.suffix, ranges_that_fill(a.suffix, suffix_items, resident * cus), &a.suffix_splits, &a.suffix_span);
+    // a wave a row where the rows' waves fill the device and their ranges are
+    // few, else a workgroup a row (4096 rows of up to 11 ranges 8.6 / 11.3 us,
+    // 3840 of 9 6.2 / 9.2; 1024 rows of 36 ranges 15 / 8)
+    const int64_t parts = a.prefix_splits + a.suffix_splits;
+    a.four = (a.rows >= 4 * cus && parts <= 12) || (a.rows >= 16 * cus && parts <= 64);
 }
 
 int64_t part_bytes(const Args &a)
@@ -1130,7 +1186,7 @@ int launch(const Args &a, hipStream_t st)
     const int64_t items =
         a.prefix_places + places(a.suffix_tiles, (int64_t)a.batch * a.kv_heads * a.suffix_splits);
     const int64_t finish =
-        a.rows + (KIND == kCache ? (int64_t)a.batch * a.kv_heads * ceil_div(a.suffix, kWeighKeys) : 0);
+        (a.four ? ceil_div(a.rows, kWaves) : a.rows) + (KIND == kCache ? (int64_t)a.batch * a.kv_heads * ceil_div(a.suffix, kWeighKeys) : 0);
     if (items > 0x7fffffffll || finish > 0x7fffffffll)
         return df11::fail(DF11_E_ARG, "attention: too many rows and keys for one launch");
     const dim3 block(64 * kWaves);
