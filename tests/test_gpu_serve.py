@@ -94,6 +94,61 @@ def test_prefix_attention_many_rows_long_prefix():
     _check_prefix(_prefix_case(5, 37, 1, 2500, [1 + (7 * i) % 90 for i in range(37)], 8, 2, 128, BF, 16), "37 x 2500")
 
 
+@pytest.mark.parametrize("B,T,P,S,Hq,H,D", [(33, 4, 40, 20, 8, 2, 64), (5, 1, 32768, 9, 64, 16, 8), (2, 1, 5000, 1100, 2, 1, 128)])
+def test_prefix_attention_row_counts_and_ranges(B, T, P, S, Hq, H, D):
+    """Enough rows for four to a joining workgroup; a prefix that is nearly
+    all there is; few rows of many ranges."""
+    _check_prefix(_prefix_case(B + P, B, T, P, [T + (i * 7) % (S - T + 1) for i in range(B)], Hq, H, D, BF, S=S),
+                  (B, T, P, S, Hq, H, D))
+
+
+def test_offsets_past_32_bits():
+    """Pages, sequences and slots whose elements lie more than 2^32 bytes and
+    2^31 elements into their tensors."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    pages = 140_000   # of 16 positions, 8 heads, 128 dims: 2.3e9 elements
+    x = _prefix_case(14, 2, 1, 30, [40, 33], 16, 8, 128, BF, 16, S=48)
+    k, v = (torch.empty((pages, 16, 8, 128), dtype=BF, device="cuda") for _ in range(2))
+    table = x["table"].clone()
+    for i, p in enumerate(x["table"].flatten().tolist()):
+        at = pages - 1 - i
+        k[at], v[at] = x["k"][p].cuda(), x["v"][p].cuda()
+        table.view(-1)[i] = at
+    out, lse = serve.prefix_attention(x["q"].cuda(), x["pk"].cuda(), x["pv"].cuda(), k, v, x["lengths"].cuda(),
+                                      block_table=table.cuda(), return_lse=True)
+    want, want_lse, bound = ref.prefix_attention(x["q"], x["pk"], x["pv"], x["k"], x["v"], x["lengths"], x["table"])
+    _close(out, want, bound, "pages")
+    _lse_close(lse, want_lse)
+    # the same memory as caches of two sequences, the second 2^31 elements behind the first
+    y = _cache_case(15, 2, 2, 70, 128, [70, 70], more=5)
+    far = 1 << 31
+    flat_k, flat_v = k.view(-1), v.view(-1)
+    strides = (far, 70 * 128, 128, 1)
+    ck, cv = (t.as_strided((2, 2, 70, 128), strides) for t in (flat_k, flat_v))
+    ck.copy_(y["k"])
+    cv.copy_(y["v"])
+    cache = serve.BoundedCache(ck, cv, y["weights"].cuda(), y["positions"].cuda(), y["lengths"].cuda())
+    q, pos = _randn(_gen(8), 2, 1, 4, 128), torch.tensor([75, 74], dtype=torch.int32)
+    cut, kept = serve.cache_compact(cache, pos.cuda(), 20, 4)
+    assert torch.equal(kept.cpu(), ref.cache_compact(y["positions"], y["weights"], y["lengths"], pos, 20, 4))
+    rows = kept.cpu().long().unsqueeze(-1).expand(2, 2, 20, 128)
+    assert torch.equal(cut.k.cpu(), y["k"].gather(2, rows)) and torch.equal(cut.v.cpu(), y["v"].gather(2, rows))
+    want, want_w, bound = ref.cache_attention(q, pos=pos, **y)
+    _close(serve.cache_attention(q.cuda(), cache, pos.cuda()), want, bound, "cache")
+    _close(cache.weights, want_w, 2.0 ** -12 * (want_w - y["weights"].double()) + 2.0 ** -22 * want_w, "weights")
+    window = _randn(_gen(9), 2, 20, 4, 128)
+    want, _, bound = ref.cache_attention(window, pos=pos - 19, **y)
+    _close(serve.cache_attention(window.cuda(), cache, pos.cuda() - 19), want, bound, "window")
+    slots, _ = ref.cache_insert(y["positions"], cache.weights.cpu(), y["lengths"], pos, 4)
+    row = _randn(_gen(10), 2, 2, 128)
+    got, _ = serve.cache_insert(cache, row.cuda(), row.cuda(), pos.cuda(), 4)
+    assert torch.equal(got.cpu(), slots)
+    for b in range(2):
+        for h in range(2):
+            assert torch.equal(ck[b, h, int(slots[b, h])].cpu(), row[b, h])
+
+
 def test_prefix_attention_empty_rows_and_scale():
     """No prefix: query tokens before the first own position see nothing."""
     x = _prefix_case(6, 4, 3, 0, [0, 1, 2, 3], 4, 2, 64, BF, S=8)
@@ -206,7 +261,7 @@ def _cuda_cache(x):
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("B,T,C,Hq,H,D", [
     (1, 1, 1, 1, 1, 8), (2, 1, 33, 8, 2, 128), (3, 1, 300, 4, 4, 64), (2, 5, 129, 6, 2, 96), (1, 20, 260, 8, 1, 128),
-    (2, 1, 1500, 7, 1, 256), (2, 2, 64, 40, 2, 80), (2, 33, 2100, 8, 2, 128), (1, 70, 1030, 4, 1, 256), (3, 40, 90, 2, 2, 64)])
+    (2, 1, 1500, 7, 1, 256), (2, 2, 64, 40, 2, 80), (2, 33, 2100, 8, 2, 128), (1, 70, 1030, 4, 1, 256), (3, 40, 90, 2, 2, 64), (40, 4, 50, 8, 2, 64)])
 def test_cache_attention(B, T, C, Hq, H, D, dtype):
     print("case", (B, T, C, Hq, H, D, dtype), flush=True)
     x = _cache_case(B + C + D, B, H, C, D, [C - (i * C) // (2 * B) for i in range(B)], dtype, more=9)
@@ -292,7 +347,8 @@ def test_cache_attention_window_with_values_that_are_no_numbers(T, Hq, H, D, C, 
 @pytest.mark.parametrize("B,H,C,D,lengths,pos,recent", [
     (1, 1, 1, 8, [0], [0], 1), (1, 1, 1, 8, [1], [5], 1), (2, 3, 40, 64, [40, 40], [49, 49], 8),
     (3, 2, 300, 128, [300, 17, 299], [320, 17, 299], 30), (2, 2, 64, 80, [64, 64], [40, -1], 0),
-    (1, 2, 500, 256, [500], [520], 500), (2, 1, 33, 72, [33, 33], [60, 60], 10 ** 10)])
+    (1, 2, 500, 256, [500], [520], 500), (2, 1, 33, 72, [33, 33], [60, 60], 10 ** 10),
+    (1, 2, 9001, 8, [9001], [9010], 40)])
 def test_cache_insert(B, H, C, D, lengths, pos, recent):
     x = _cache_case(C + D, B, H, C, D, lengths, more=20)
     if C > 30:
@@ -341,7 +397,8 @@ def test_cache_insert_takes_stale_slots_first_and_fills_by_weight():
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("B,H,C,D,lengths,budget,recent,slots", [
     (1, 1, 1, 8, [1], 1, 0, 1), (2, 2, 100, 64, [100, 60], 40, 10, 40), (2, 1, 2500, 128, [2500, 1030], 1025, 1025, 1100),
-    (3, 2, 300, 80, [300, 20, 0], 64, 0, 70), (1, 3, 5000, 256, [4999], 700, 33, 700)])
+    (3, 2, 300, 80, [300, 20, 0], 64, 0, 70), (1, 3, 5000, 256, [4999], 700, 33, 700), (1, 2, 70001, 8, [70000], 9000, 100, 9000),
+    (1, 1, 12000, 8, [12000], 50, 0, 50)])
 def test_cache_compact(B, H, C, D, lengths, budget, recent, slots, dtype):
     x = _cache_case(C + D, B, H, C, D, lengths, dtype, more=7)
     if C >= 100:
@@ -387,7 +444,7 @@ def _check_verify(x, counts=None):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF, HF])
-@pytest.mark.parametrize("B,G,V", [(1, 1, 1), (3, 0, 7), (8, 3, 33), (4, 5, 1000), (6, 4, 5003), (2, 7, 40000)])
+@pytest.mark.parametrize("B,G,V", [(1, 1, 1), (3, 0, 7), (8, 3, 33), (4, 5, 1000), (6, 4, 5003), (2, 7, 40000), (1, 2, 600011)])
 def test_verify_drafts(B, G, V, dtype):
     print("case", (B, G, V, dtype), flush=True)
     x = _verify_case(B + G + V, B, G, V, dtype)
