@@ -64,6 +64,8 @@ def _elsewhere(t, stream) -> bool:
 def _there(t, stream):
     """The context in which a call's device and stream are the current ones
     (its outputs and workspaces belong to that stream)."""
+    if stream is not None and stream.device != t.device:
+        raise ValueError("the stream is of %s, the operands are on %s" % (stream.device, t.device))
     return torch.cuda.device(t.device) if stream is None else torch.cuda.stream(stream)
 
 
