@@ -67,6 +67,7 @@ struct Args {
     int32_t prefix_splits, prefix_span, prefix_tiles, suffix_splits, suffix_span, suffix_tiles;
     int64_t prefix_places;     // workgroups of the prefix
     int64_t rows;              // batch * tokens * heads
+    int32_t weigh_run;         // many rows: slots of a workgroup that weighs
     bool big;                  // tiles of 128 rows
     bool four;                 // four output rows to a joining workgroup
 };
@@ -952,14 +953,39 @@ __device__ __forceinline__ void weigh_block(const Args &a, int bh, int first)
     if (first >= n) return;
     const int key = first + 4 * threadIdx.x;
     const int row_count = a.tokens * a.group, parts = own_splits(a, b), wave = threadIdx.x >> 6;
+    const auto row_of = [&](int r) {
+        return ((int64_t)b * a.tokens + r / a.group) * a.heads + head * a.group + r % a.group;
+    };
     float w[4] = {0, 0, 0, 0};
     for (int r0 = 0; r0 < row_count; r0 += 64) {
         const int some = min(64, row_count - r0);
         __syncthreads();
-        for (int r = wave; r < some; r += kWaves) {
-            const int t = (r0 + r) / a.group, h = (r0 + r) % a.group;
-            const float2 ml = join_row(a, ((int64_t)b * a.tokens + t) * a.heads + head * a.group + h, parts);
-            if ((threadIdx.x & 63) == 0) top[r] = ml.y == 0.0f ? INFINITY : ml.x + __log2f(ml.y);   // an empty row gives nothing
+        // many ranges: a wave a row; few: four lanes a row, all rows at once
+        // (28 rows of one range: 13.7 us for the launch with a wave a row)
+        if (parts > 16) {
+            for (int r = wave; r < some; r += kWaves) {
+                const float2 ml = join_row(a, row_of(r0 + r), parts);
+                if ((threadIdx.x & 63) == 0) top[r] = ml.y == 0.0f ? INFINITY : ml.x + __log2f(ml.y);
+            }
+        } else {
+            const int r = threadIdx.x / 4;
+            const int64_t row = row_of(r0 + min(r, some - 1));
+            float m = -INFINITY, l = 0.0f;
+            float2 x[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int s = (threadIdx.x & 3) + 4 * j;
+                x[j] = s < parts ? a.part_ml[s * a.rows + row] : make_float2(-INFINITY, 0.0f);
+                m = fmaxf(m, x[j].x);
+            }
+            m = fmaxf(m, __shfl_xor(m, 1));
+            m = fmaxf(m, __shfl_xor(m, 2));
+            const float safe = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+            for (int j = 0; j < 4; j++) l += exp2_fast(x[j].x - safe) * x[j].y;
+            l += __shfl_xor(l, 1);
+            l += __shfl_xor(l, 2);
+            if (r < some && (threadIdx.x & 3) == 0) top[r] = l == 0.0f ? INFINITY : m + __log2f(l);   // an empty row gives nothing
         }
         __syncthreads();
         if (key < n) {
@@ -984,14 +1010,13 @@ __device__ __forceinline__ void weigh_block(const Args &a, int bh, int first)
 // logits with 32 rows between them.  128 rows, 4 x 8 heads of 16384 slots: 46
 // us, 17 GFLOP and 134 MB (kept logits would be 268 MB to write and to read).
 constexpr int kWeighRows = 128;
-constexpr int kTileKeys = 512;   // slots of a workgroup
 
 template <class E, int DP>
 __global__ void __launch_bounds__(64 * kWaves, 2) weigh_kernel(const Args a)
 {
     typedef TileShape<DP> S;
     __shared__ alignas(1024) char lds[kWeighRows * (DP * 2 + 8)];
-    const int bh = blockIdx.y, first = blockIdx.x * kTileKeys;
+    const int bh = blockIdx.y, first = blockIdx.x * a.weigh_run;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31, g = lane >> 5;
     const int b = bh / a.kv_heads, head = bh % a.kv_heads;
     const int n = max(0, min(a.lengths[b], a.suffix));
@@ -1032,7 +1057,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) weigh_kernel(const Args a)
             }
             next_place = base + c < n ? places[key] : -1;
         };
-        const int end = min(n, first + kTileKeys);
+        const int end = min(n, first + a.weigh_run);
         load(first + 32 * wave);
         for (int base = first + 32 * wave; base < end; base += 32 * kWaves) {
             const int key = base + c;
@@ -1154,6 +1179,11 @@ void plan(Args &a, bool cache)
     const int64_t suffix_items = (int64_t)a.suffix_tiles * a.kv_heads * a.batch;
     a.prefix_places = a.prefix_splits ? places(a.prefix_tiles, (int64_t)a.kv_heads * a.prefix_splits) : 0;
     set_ranges(a.suffix, ranges_that_fill(a.suffix, suffix_items, resident * cus), &a.suffix_splits, &a.suffix_span);
+    // the slots of a workgroup that weighs many rows: 512, whose rows' queries
+    // are brought to LDS once, or fewer where that leaves most CUs idle (28
+    // tokens over 872 slots of 3 prompts: 15.8 us in runs of 512, 8.4 of 128)
+    a.weigh_run = 512;
+    while (a.weigh_run > 128 && (int64_t)a.batch * a.kv_heads * ceil_div(a.suffix, a.weigh_run) < 2 * cus) a.weigh_run /= 2;
     // a wave a row where the rows' waves fill the device and their ranges are
     // few, else a workgroup a row (4096 rows of up to 11 ranges 8.6 / 11.3 us,
     // 3840 of 9 6.2 / 9.2; 1024 rows of 36 ranges 15 / 8)
@@ -1209,7 +1239,7 @@ int launch(const Args &a, hipStream_t st)
     if (items) hipLaunchKernelGGL((attend_kernel<E, DP, KIND>), dim3((uint32_t)items), block, 0, st, a);
     hipLaunchKernelGGL((finish_kernel<E, KIND == kCache>), dim3((uint32_t)finish), block, 0, st, a);
     if constexpr (KIND == kCacheTiles) {
-        const dim3 grid(ceil_div(a.suffix, kTileKeys), a.batch * a.kv_heads);
+        const dim3 grid(ceil_div(a.suffix, a.weigh_run), a.batch * a.kv_heads);
         if (a.suffix) hipLaunchKernelGGL((weigh_kernel<E, DP>), grid, block, 0, st, a);
     }
     const hipError_t e = hipGetLastError();

@@ -135,7 +135,7 @@ __device__ __forceinline__ void pick(const uint32_t *bins, int each, uint32_t le
 // before it.  What the slots hold is moved by move_kernel: here that would
 // wait for memory once for each of a lane's N.  A cache of more than 1024 N
 // slots is taken in rounds, whose worths are computed again for each pass.
-// 3001 slots 12 us (2 to read them), 128 heads of 32768 slots 34 us (9 to
+// 3001 slots 10.8 us (2 to read them), 128 heads of 32768 slots 34 us (9 to
 // read, 7 to write the indexes): latency of the passes' barriers and of the
 // bins' LDS atomics.
 template <int N>
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const Cache c, c
     bool sought = true;
     for (int pass = 0; pass < 3 && sought; pass++) {
         const int low = pass == 0 ? 20 : pass == 1 ? 10 : 0, high = pass == 0 ? 32 : low + 10;
-        for (int i = threadIdx.x; i < kBins; i += kSelectThreads) bins[i] = 0;
+        for (int i = threadIdx.x; i < 1 << (high - low); i += kSelectThreads) bins[i] = 0;
         if (pass == 0 && threadIdx.x < 2) total[threadIdx.x] = 0;
         __syncthreads();
         uint32_t late = 0, others = 0;
@@ -332,13 +332,16 @@ extern "C" int df11_cache_compact(const df11_cache *cache, const int32_t *pos, i
     if (c.slots && (out.k == c.k || out.v == c.v || out.weights == c.weights || out.positions == c.positions))
         return df11::fail(DF11_E_ARG, "%s: a cache is not cut down in place", who);
     hipStream_t st = (hipStream_t)stream;
-    const dim3 heads(c.batch * c.kv_heads), threads(kSelectThreads);
-    if (c.slots <= 8 * kSelectThreads)
-        hipLaunchKernelGGL(select_kernel<8>, heads, threads, 0, st, c, pos, (int32_t)budget, recent, out.slots,
-                           kept, out_lengths);
-    else
-        hipLaunchKernelGGL(select_kernel<32>, heads, threads, 0, st, c, pos, (int32_t)budget, recent, out.slots,
-                           kept, out_lengths);
+    const auto select = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(c.batch * c.kv_heads), dim3(kSelectThreads), 0, st, c, pos, (int32_t)budget, recent,
+                           out.slots, kept, out_lengths);
+    };
+    // as few slots of a lane as hold the cache in one round (3001 slots 10.8 us
+    // with 4, 12 with 8; 14054 slots 16.8 us with 16, 23 with 32)
+    if (c.slots <= 4 * kSelectThreads) select(select_kernel<4>);
+    else if (c.slots <= 8 * kSelectThreads) select(select_kernel<8>);
+    else if (c.slots <= 16 * kSelectThreads) select(select_kernel<16>);
+    else select(select_kernel<32>);
     hipLaunchKernelGGL(move_kernel, dim3((out.slots + 15) / 16, c.batch * c.kv_heads), dim3(256), 0, st, c, out, kept);
     return launched(who);
 }
