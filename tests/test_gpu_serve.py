@@ -313,6 +313,30 @@ def test_cache_attention_later_tokens_do_not_reach_earlier_ones():
     _close(c.weights, want_w, 2.0 ** -12 * (want_w - x["weights"].double()) + 2.0 ** -22 * want_w, "weights")
 
 
+@pytest.mark.parametrize("T,Hq,H,D,C", [(1, 2, 1, 64, 40), (3, 4, 2, 128, 700), (3, 4, 2, 128, 5000), (40, 2, 2, 128, 300), (70, 2, 1, 64, 150)])
+def test_cache_attention_a_query_that_is_no_number_reaches_only_slots_it_sees(T, Hq, H, D, C):
+    """One head's query of one token is NaN: its row, and the weights of the slots it sees, are; no others."""
+    x = _cache_case(T + C, 2, H, C, D, [C, C - 3], more=6)
+    pos = torch.tensor([C + 4 - T, C // 2], dtype=torch.int32)
+    q = _randn(_gen(T), 2, T, Hq, D)
+    clean = q.clone()
+    bad = T // 3
+    q[:, bad, Hq - 1] = NAN
+    want, want_w, bound = ref.cache_attention(clean, pos=pos, **x)
+    c = _cuda_cache(x)
+    out = serve.cache_attention(q.cuda(), c, pos.cuda()).cpu()
+    assert bool(torch.isnan(out[:, bad, Hq - 1]).all())
+    out[:, bad, Hq - 1] = want[:, bad, Hq - 1].to(out.dtype)
+    _close(out, want, bound, "other rows")
+    there = torch.arange(C) < x["lengths"].view(-1, 1, 1)
+    reached = there & (x["positions"] <= pos.view(-1, 1, 1) + bad) & (torch.arange(H).view(1, -1, 1) == H - 1)
+    got = c.weights.cpu()
+    assert bool((~there | (x["positions"] > pos.view(-1, 1, 1) + bad)).any())
+    assert torch.equal(torch.isnan(got), reached)
+    got[reached] = want_w[reached].to(got.dtype)
+    _close(got, want_w, 2.0 ** -12 * (want_w - x["weights"].double()) + 2.0 ** -22 * want_w, "weights")
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("bad", [NAN, INF, -INF])
 @pytest.mark.parametrize("T,Hq,H,D,C", [(24, 4, 2, 128, 300), (40, 1, 1, 64, 150), (33, 4, 4, 256, 70), (9, 8, 2, 72, 129)])
