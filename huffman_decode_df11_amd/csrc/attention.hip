@@ -994,7 +994,10 @@ __device__ __forceinline__ void weigh_block(const Args &a, int bh, int first)
             for (int i = 0; i < some; i++) {
                 const f32x4 s = *(const f32x4 *)(from + i * a.logit_stride);
 #pragma unroll
-                for (int j = 0; j < 4; j++) w[j] += s[j] == -INFINITY ? 0.0f : exp2_fast(s[j] - top[i]);   // unseen: also where the row's sum is NaN
+                for (int j = 0; j < 4; j++) {
+                    const float p = exp2_fast(s[j] - top[i]);
+                    w[j] += s[j] == -INFINITY ? 0.0f : p;   // an unseen slot's is 0 also where the row's sum is NaN
+                }
             }
         }
     }
