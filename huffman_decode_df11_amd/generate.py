@@ -205,6 +205,8 @@ class Generator:
         uniforms = torch.rand((self.batch, self.drafts + 1), generator=self.random, device=p.device)
         tokens, taken = serve.verify_drafts(drafts, p, uniforms, q)
         self.own_count = self.own_count + taken + 1
+        for cache in self.caches:
+            cache.forget(self._positions())   # the refused drafts, before their positions are taken by others
         self.last = torch.gather(tokens, 1, taken[:, None].long())[:, 0]
         return tokens, taken
 

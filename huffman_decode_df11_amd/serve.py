@@ -127,6 +127,24 @@ class BoundedCache:
         """The slots in use from now on (what cache_insert returned)."""
         self.lengths.copy_(lengths)
 
+    def forget(self, pos, *, stream=None) -> None:
+        """Tokens taken back, in place: every slot whose position is pos[b] or
+        more holds no token from now on (pos [B] int32, the sequence's next
+        position; a negative one: that sequence keeps all).  To be called
+        whenever drafts that were inserted are refused: left as they are,
+        they would be seen again, beside the tokens that took their
+        positions, as soon as the sequence has passed them.  The weights that
+        the refused tokens' queries gave other slots stay."""
+        if _elsewhere(self.k, stream):
+            with _there(self.k, stream):
+                return self.forget(pos)
+        if not isinstance(pos, torch.Tensor) or pos.dtype != torch.int32:
+            raise TypeError("pos must be an int32 tensor")
+        if pos.device != self.positions.device or tuple(pos.shape) != (self.shape[0],):
+            raise ValueError("pos must be [%d] on %s" % (self.shape[0], self.positions.device))
+        at = pos.view(-1, 1, 1)
+        self.positions.masked_fill_((self.positions >= at) & (at >= 0), NO_TOKEN)
+
 
 def cache_attention(q, cache: BoundedCache, pos, *, scale: Optional[float] = None, out=None, stream=None):
     """Attention of q [B, T, Hq, D] over a bounded cache.  Query token t of
@@ -144,8 +162,10 @@ def cache_insert(cache: BoundedCache, k_new, v_new, pos, recent: int, *, stream=
     """One token into every sequence's cache, in place: k_new, v_new
     [B, Hkv, D] at position pos[b] (pos [B] int32; a negative one: no token
     for that sequence).  While a sequence uses fewer than `slots` slots the
-    next one is taken, then a stale one, then the one of least weight among
-    those outside the `recent` latest positions.  Returns the slots taken
+    next one is taken, then the first stale one (without a token, or at pos[b]
+    or past it), then the one of least weight among those outside the `recent`
+    latest positions.  No other slot changes: BoundedCache.forget gives up
+    tokens that were taken back.  Returns the slots taken
     [B, Hkv] (-1: none) and the new lengths [B], both int32; cache.lengths
     is left as it is (set_lengths)."""
     if _elsewhere(cache.k, stream):

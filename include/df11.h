@@ -502,9 +502,13 @@ int df11_prefix_attention(const df11_prefix_attention_args *a, void *workspace, 
 /* A bounded cache: for each sequence and key head `slots` slots of a key, a
  * value, the attention weight the slot has gathered and the position of its
  * token.  Sequence b uses the slots [0, lengths[b]).  A slot whose position
- * is DF11_NO_TOKEN (or negative) holds none; one whose position is at or past the
- * sequence's next position (a refused draft) is stale: neither is seen, and
- * they are the first to be replaced. */
+ * is DF11_NO_TOKEN (or negative) holds none: it is not seen, and is the first
+ * to be replaced.  So is one whose position is at or past the sequence's next
+ * position, but only until the sequence has passed that position: then it
+ * counts as seen, beside any other slot of the same position.  A caller that
+ * takes tokens back (refused drafts) sets the positions of their slots to
+ * DF11_NO_TOKEN before the next token is inserted.  Weights that the queries
+ * of such tokens gave to other slots stay. */
 typedef struct df11_cache {
     void *k, *v;                  /* [batch, kv_heads, slots, dim] */
     float *weights;               /* [batch, kv_heads, slots], contiguous */
@@ -538,7 +542,8 @@ int df11_cache_attention(const df11_cache *c, const df11_cache_attention_args *a
  * (the `recent` latest positions, the new one among them, are kept), the
  * one of least weight, the lowest of equals (a NaN weight counts as less
  * than any); and if there is none, the slot of the lowest position.  A
- * sequence with pos[b] < 0 takes no token.  out_slots [batch, kv_heads]: the slot taken, or
+ * sequence with pos[b] < 0 takes no token.  No other slot is written: stale
+ * ones that are left keep their positions (df11_cache above).  out_slots [batch, kv_heads]: the slot taken, or
  * -1.  out_lengths [batch]: min(lengths[b] + 1, slots), lengths[b] for a
  * sequence that takes none (lengths itself is not written; out_lengths must
  * be another array).  Errors: as df11_prefix_attention. */

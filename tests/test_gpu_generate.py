@@ -82,3 +82,27 @@ def test_command():
         generate.main()
     finally:
         sys.argv = argv
+
+
+@pytest.mark.parametrize("prompt,budget,drafts,seed", [(100, 48, 4, 8), (100, 48, 4, 9), (40, 200, 4, 10), (100, 64, 3, 11)])
+def test_refused_drafts_leave_the_bounded_caches(prompt, budget, drafts, seed, monkeypatch):
+    """After every round, full caches and not full ones: no position twice and
+    none from behind the tokens that stay.  About half of the drafts are
+    refused (the drafter's probabilities are doubled before the verification)."""
+    verify = serve.verify_drafts
+    monkeypatch.setattr(generate.serve, "verify_drafts", lambda d, p, u, q: verify(d, p, u, 2.0 * q))
+    model = generate.Decoder(generate.Config(vocab=1024), seed=6)
+    ids = torch.randint(1024, (prompt,), generator=torch.Generator().manual_seed(7))
+    g = generate.Generator(model, ids, batch=4, budget=budget, recent=12, drafts=drafts, room=120, temperature=1.0, seed=seed)
+    refused = 0
+    for _ in range(12):
+        _, taken = g.round()
+        refused += int((drafts - taken).sum())
+        nxt = g._positions().cpu()
+        for cache in g.caches:
+            for b in range(4):
+                for h in range(model.config.kv_heads):
+                    there = cache.positions[b, h, :int(cache.lengths[b])].tolist()
+                    there = [p for p in there if p != serve.NO_TOKEN]
+                    assert len(there) == len(set(there)) and max(there) < int(nxt[b])
+    assert refused > 40

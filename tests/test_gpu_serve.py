@@ -680,3 +680,72 @@ def test_refusals():
     with pytest.raises(TypeError):
         serve.verify_drafts(z(2, 3, dtype=torch.int32, device="cuda"), z(2, 4, 50, device="cuda"), z(2, 4, device="cuda"),
                             z(2, 3, 50, dtype=BF, device="cuda"))
+
+
+@pytest.mark.parametrize("C,used,recent", [(24, 24, 4), (40, 24, 4), (16, 16, 16)])
+def test_refused_drafts_are_not_seen_again(C, used, recent):
+    """Rounds of drafts into full and not full caches, a full one's in slots of
+    descending index, all or some of them refused and forgotten: after each
+    insertion the attention is that over the tokens that were kept, held
+    beside the cache by their positions."""
+    B, H, D, drafts = 2, 2, 64, 4
+    x = _cache_case(41 + C, B, H, C, D, [used] * B)
+    for b in range(B):
+        for h in range(H):
+            x["positions"][b, h, :used] = torch.randperm(used, generator=_gen(2 * b + h))
+    x["positions"][:, :, used:] = ref.NO_TOKEN
+    x["weights"] = torch.arange(C, 0, -1, dtype=torch.float32).expand(B, H, C).contiguous()   # the last slot is the lightest
+    c = _cuda_cache(x)
+    held = {(b, h): {int(x["positions"][b, h, i]): (i, x["k"][b, h, i], x["v"][b, h, i]) for i in range(used)}
+            for b in range(B) for h in range(H)}
+    g, nxt = _gen(5), [used] * B
+    for turn in range(8):
+        for step in range(drafts):
+            pos = torch.tensor([n + step for n in nxt], dtype=torch.int32)
+            k_new, v_new = _randn(g, B, H, D), _randn(g, B, H, D)
+            slots, lengths = serve.cache_insert(c, k_new.cuda(), v_new.cuda(), pos.cuda(), recent)
+            c.set_lengths(lengths)
+            for (b, h), tokens in held.items():
+                for p in [p for p, t in tokens.items() if t[0] == int(slots[b, h])]:
+                    del tokens[p]
+                assert int(pos[b]) not in tokens
+                tokens[int(pos[b])] = (int(slots[b, h]), k_new[b, h], v_new[b, h])
+            q = _randn(g, B, 1, 2 * H, D)
+            out = serve.cache_attention(q.cuda(), c, pos.cuda()).cpu()
+            for b in range(B):
+                for head in range(2 * H):
+                    tokens = held[b, head // 2].values()
+                    want, _, _, bound = ref.attend(q[b, 0, head], torch.stack([t[1] for t in tokens]),
+                                                   torch.stack([t[2] for t in tokens]), D ** -0.5)
+                    _close(out[b, 0, head], want, bound, (turn, step, b, head))
+            # weights as the caller likes them: the least in the last slot, so that evictions go downwards
+            c.weights.copy_(x["weights"])
+        kept = [(turn * 3 + b) % drafts for b in range(B)]   # none, some, all but one
+        nxt = [n + k for n, k in zip(nxt, kept)]
+        c.forget(torch.tensor(nxt, dtype=torch.int32, device="cuda"))
+        for (b, h), tokens in held.items():
+            for p in [p for p in tokens if p >= nxt[b]]:
+                del tokens[p]
+            live = c.positions[b, h, :int(c.lengths[b])].cpu()
+            assert sorted(tokens) == sorted(live[live != ref.NO_TOKEN].tolist())
+
+
+def test_forget():
+    """Other sequences, a negative position, the arguments."""
+    x = _cache_case(43, 3, 2, 30, 64, [30, 20, 30])
+    c = _cuda_cache(x)
+    c.forget(torch.tensor([10, 25, -1], dtype=torch.int32, device="cuda"))
+    want = x["positions"].clone()
+    for b, n in ((0, 10), (1, 25)):
+        want[b][want[b] >= n] = ref.NO_TOKEN
+    assert torch.equal(c.positions.cpu(), want)
+    for n in ("k", "v", "weights", "lengths"):
+        assert torch.equal(getattr(c, n).cpu(), x[n]), n
+    with pytest.raises(TypeError):
+        c.forget(torch.tensor([10, 25, -1], device="cuda"))
+    with pytest.raises(TypeError):
+        c.forget(10)
+    with pytest.raises(ValueError):
+        c.forget(torch.tensor([10, 25], dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        c.forget(torch.tensor([10, 25, 3], dtype=torch.int32))
