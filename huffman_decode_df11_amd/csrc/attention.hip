@@ -386,6 +386,11 @@ __device__ __forceinline__ void attend_wave(const Src &src, const u32x4 (&q)[DP 
 // the time, one phase of a step behind the other.
 constexpr int kTileRows = 32 * kWaves;
 
+// Rows up to this many elements apart go into 128-row tiles: a lane's distance
+// spans up to 124 of them (dims to 64) in a 32-bit number.  16-row tiles, whose
+// lanes span 15, take the others.
+constexpr int64_t kTileStride = 1ll << 25;
+
 template <int DP>
 struct TileShape {
     static constexpr int kKeys = 8192 / DP;          // keys of a step: 16 KB of K and of V
@@ -461,11 +466,11 @@ __device__ __forceinline__ void tile_block(const Args &a, char *lds, int seq, in
     // at a uniform address plus its own 32-bit distance.
     u32x4 kx[4], vx[4];
     const int v_quad = threadIdx.x / S::kChunks, v_chunk = threadIdx.x % S::kChunks;
-    const int32_t token = (int32_t)kv_token;
+    const uint32_t token = (uint32_t)kv_token;
     int32_t place[4];
     const int my_d = v_chunk * 8 < a.dim ? v_chunk * 8 : 0;
     const bool pad = v_chunk * 8 >= a.dim;   // dims that K does not have take part as 0
-    const uint32_t k_far = (uint32_t)(v_quad * token) + my_d, v_far = (uint32_t)(4 * v_quad * token) + my_d;
+    const uint32_t k_far = v_quad * token + my_d, v_far = 4 * v_quad * token + my_d;   // below 2^32: kTileStride
     constexpr int kRowsEach = 256 / S::kChunks;   // keys between a thread's chunks of K
     const auto load = [&](int base) {
         if (base + kKeys <= key1) {
@@ -1167,7 +1172,7 @@ void plan(Args &a, bool cache)
     // rows, is the less (us in 16- / 128-row tiles: 8191 shared positions 15.4
     // / 17.8 at 16 rows, 19.1 / 17.3 at 24, 23.4 / 18.7 at 64; caches of 16384
     // slots 99 / 117 at 32 rows, 135 / 120 at 48, 167 / 121 at 64).
-    a.big = cache ? own_rows > 32 : shared_rows > 16;
+    a.big = cache ? own_rows > 32 && a.k_token <= kTileStride : shared_rows > 16 && a.prefix_token <= kTileStride;
     a.prefix_tiles = ceil_div(shared_rows, a.big ? kTileRows : kRows);
     a.suffix_tiles = ceil_div(own_rows, cache && a.big ? kTileRows : kRows);
     // 128-row tiles: one workgroup on each CU, whose partial sums are few and
@@ -1223,7 +1228,7 @@ int strides_ok(const char *who, std::initializer_list<int64_t> strides, std::ini
 {
     for (int64_t s : strides)
         if (s < 0 || s % 8) return df11::fail(DF11_E_ARG, "%s: stride %lld is not a multiple of 8", who, (long long)s);
-    // a lane's distance within 16 rows is a 32-bit number
+    // the distance of a 16-row tile's lane, within 15 rows, is a 32-bit number
     for (int64_t s : rows)
         if (s >= 1ll << 27) return df11::fail(DF11_E_ARG, "%s: rows %lld elements apart", who, (long long)s);
     return DF11_OK;

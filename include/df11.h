@@ -493,8 +493,8 @@ uint64_t df11_prefix_attention_workspace_bytes(const df11_prefix_attention_args 
 /* workspace: 16-byte aligned, at least that many bytes, not used by other
  * work until this call's work has finished; its contents need no clearing.
  * The result does not depend on the run.  Errors: E_ARG (null or misaligned
- * pointer -- 16 bytes for q, k, v and out, strides multiples of 8 -- sizes out of
- * range, dim not a multiple of 8 or above DF11_MAX_DIM, heads not a
+ * pointer -- 16 bytes for q, k, v and out, strides multiples of 8, those between
+ * a head's keys below 2^27 -- sizes out of range, dim not a multiple of 8 or above DF11_MAX_DIM, heads not a
  * multiple of kv_heads, scale not positive, workspace too small), E_DEVICE. */
 int df11_prefix_attention(const df11_prefix_attention_args *a, void *workspace, uint64_t workspace_bytes,
                           void *stream);

@@ -749,3 +749,37 @@ def test_forget():
         c.forget(torch.tensor([10, 25], dtype=torch.int32, device="cuda"))
     with pytest.raises(ValueError):
         c.forget(torch.tensor([10, 25, 3], dtype=torch.int32))
+
+
+@pytest.mark.parametrize("D,token", [(64, 1 << 25), (64, 34_700_000), (128, 1 << 25), (128, 71_600_000), (72, (1 << 27) - 8)])
+def test_rows_far_apart(D, token):
+    """Many rows over keys whose rows lie `token` elements apart: at the most
+    that 128-row tiles take, where a tile's lane distance (124 or 60 rows)
+    passes 2^32 elements, and at the most that any call takes."""
+    n = min(2 * 8192 // 64 if D == 64 else 8192 // 64, 6_000_000_000 // token)   # keys: 6e9 elements at most
+    H = 2
+    if torch.cuda.mem_get_info()[0] < 2 * n * token + (8 << 30):
+        pytest.skip("needs %d GB of device memory" % (2 * n * token + (8 << 30) >> 30))
+    assert token <= 1 << 25 or n > 40
+    flat = torch.empty((n - 1) * token + 2 * H * D + 64, dtype=BF, device="cuda")
+    far_k, far_v = (flat[i * H * D:].as_strided((n, H, D), (token, D, 1)) for i in range(2))
+    g = _gen(D)
+    pk, pv = _randn(g, n, H, D), _randn(g, n, H, D)
+    far_k.copy_(pk), far_v.copy_(pv)
+    q, k, v = _randn(g, 10, 1, 4, D), _randn(g, 10, 3, H, D), _randn(g, 10, 3, H, D)   # 20 rows of a key head
+    lengths = torch.full((10,), 3, dtype=torch.int32)
+    out, lse = serve.prefix_attention(q.cuda(), far_k, far_v, k.cuda(), v.cuda(), lengths.cuda(), return_lse=True)
+    want, want_lse, bound = ref.prefix_attention(q, pk, pv, k, v, lengths)
+    _close(out, want, bound, "prefix")
+    _lse_close(lse, want_lse)
+    # the same rows as a cache's slots, under a window of 40 query tokens
+    x = dict(k=pk.transpose(0, 1)[None], v=pv.transpose(0, 1)[None], weights=torch.zeros(1, H, n),
+             positions=torch.arange(n, dtype=torch.int32).expand(1, H, n).contiguous(),
+             lengths=torch.tensor([n], dtype=torch.int32))
+    pos = torch.tensor([n - 40], dtype=torch.int32)
+    cache = serve.BoundedCache(far_k.transpose(0, 1)[None], far_v.transpose(0, 1)[None],
+                               *(x[name].cuda() for name in ("weights", "positions", "lengths")))
+    q = _randn(g, 1, 40, 2, D)
+    want, want_w, bound = ref.cache_attention(q, pos=pos, **x)
+    _close(serve.cache_attention(q.cuda(), cache, pos.cuda()), want, bound, "window")
+    _close(cache.weights, want_w, 2.0 ** -12 * want_w + 2.0 ** -22 * want_w, "weights")
