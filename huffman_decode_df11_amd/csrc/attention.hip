@@ -681,8 +681,9 @@ __device__ __forceinline__ void tile_block(const Args &a, char *lds, int seq, in
         // tokens see, times its weight for the rows that do.
         for (int base = key0; base < key1; base += 64) {
             const int32_t at = base + lane < key1 ? places[base + lane] : -1;
-            const int32_t rel = at < 0 || at <= pos ? 0 : at - pos;
-            for (uint64_t left = __ballot(rel > 0 && rel < a.tokens); left; left &= left - 1) {
+            // only where some tokens see it: at - pos of any other need not fit 32 bits
+            const int32_t rel = at > pos && (int64_t)at < (int64_t)pos + a.tokens && at >= 0 ? at - pos : 0;
+            for (uint64_t left = __ballot(rel > 0); left; left &= left - 1) {
                 const int i = __builtin_ctzll(left);
                 const uint16_t *kr = kp + (base + i) * kv_token, *vr = vp + (base + i) * kv_token;
                 float x = 0.0f;

@@ -783,3 +783,28 @@ def test_rows_far_apart(D, token):
     want, want_w, bound = ref.cache_attention(q, pos=pos, **x)
     _close(serve.cache_attention(q.cuda(), cache, pos.cuda()), want, bound, "window")
     _close(cache.weights, want_w, 2.0 ** -12 * want_w + 2.0 ** -22 * want_w, "weights")
+
+
+@pytest.mark.parametrize("first", [-3, -39, -(1 << 31)])
+def test_cache_attention_window_from_before_the_first_position(first):
+    """Many rows from a negative position on: tokens before position 0 see
+    nothing; a value that is no number at position 5 reaches the tokens from
+    there on, those of empty slots none."""
+    T, C = 40, 150
+    x = _cache_case(4, 1, 1, C, 64, [C])
+    x["positions"][0, 0] = torch.arange(C, dtype=torch.int32)
+    x["positions"][0, 0, 20:140] = ref.NO_TOKEN
+    x["v"][0, 0, 20:140] = NAN
+    clean = {n: t.clone() for n, t in x.items()}
+    clean["v"][0, 0, 20:140] = 0
+    x["v"][0, 0, 5] = NAN
+    pos = torch.tensor([first], dtype=torch.int32)
+    q = _randn(_gen(2), 1, T, 1, 64)
+    c = _cuda_cache(x)
+    out = serve.cache_attention(q.cuda(), c, pos.cuda()).cpu()
+    at = first + torch.arange(T)
+    assert torch.equal(torch.isnan(out).any(-1)[0, :, 0], at >= 5)
+    assert bool((out[0, at < 0] == 0).all())
+    want, want_w, bound = ref.cache_attention(q, pos=pos, **clean)
+    _close(out[:, at < 5], want[:, at < 5], bound[:, at < 5], "tokens before the value")
+    _close(c.weights, want_w, 2.0 ** -12 * (want_w - x["weights"].double()) + 2.0 ** -22 * want_w, "weights")
