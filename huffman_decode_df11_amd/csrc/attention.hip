@@ -54,7 +54,7 @@ enum { kRowTiles, kTiles, kCache, kCacheTiles };
 struct Args {
     const uint16_t *q, *prefix_k, *prefix_v, *k, *v;
     const int32_t *lengths, *table, *pos, *positions;
-    uint16_t *out;
+    uint16_t *out;             // NULL: only the rows' logarithms are wanted
     float *lse, *weights;
     float *part_o;             // [slot][row][dim]
     float2 *part_ml;           // [slot][row]
@@ -70,6 +70,7 @@ struct Args {
     int32_t weigh_run;         // many rows: slots of a workgroup that weighs
     bool big;                  // tiles of 128 rows
     bool four;                 // four output rows to a joining workgroup
+    bool out_on_q;             // out shares memory with q
 };
 
 // Workgroups i and i + 8 run on one of the eight dies, which has an L2 of its
@@ -900,7 +901,7 @@ __device__ __forceinline__ void join_block(const Args &a, int64_t row)
     }
     __syncthreads();
     const float inv = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
-    if (2 * threadIdx.x < a.dim) {
+    if (a.out && 2 * threadIdx.x < a.dim) {
         float x = 0.0f, y = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; w++) x += sums[w][threadIdx.x].x, y += sums[w][threadIdx.x].y;
@@ -928,7 +929,7 @@ __device__ __forceinline__ void join_wave(const Args &a, int64_t row)
 #pragma unroll
     for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    for (int d = 2 * lane; d < a.dim; d += 128) {
+    for (int d = 2 * lane; a.out && d < a.dim; d += 128) {
         float x = 0.0f, y = 0.0f;
         for (int s0 = 0; s0 < parts; s0 += 8) {
             float2 o[8];
@@ -1246,11 +1247,18 @@ int launch(const Args &a, hipStream_t st)
         return df11::fail(DF11_E_ARG, "attention: too many rows and keys for one launch");
     const dim3 block(64 * kWaves);
     if (items) hipLaunchKernelGGL((attend_kernel<E, DP, KIND>), dim3((uint32_t)items), block, 0, st, a);
-    hipLaunchKernelGGL((finish_kernel<E, KIND == kCache>), dim3((uint32_t)finish), block, 0, st, a);
+    const auto join = [&](const Args &x) {
+        hipLaunchKernelGGL((finish_kernel<E, KIND == kCache>), dim3((uint32_t)finish), block, 0, st, x);
+    };
     if constexpr (KIND == kCacheTiles) {
+        // the weights' logits are taken from q again: where out lies on it, the outputs are joined last
+        Args x = a;
+        if (a.out_on_q) x.out = nullptr;
+        join(x);
         const dim3 grid(ceil_div(a.suffix, a.weigh_run), a.batch * a.kv_heads);
         if (a.suffix) hipLaunchKernelGGL((weigh_kernel<E, DP>), grid, block, 0, st, a);
     }
+    if (KIND != kCacheTiles || a.out_on_q) join(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return df11::fail(DF11_E_DEVICE, "attention launch: %s", hipGetErrorString(e));
     return DF11_OK;
@@ -1337,6 +1345,11 @@ int make_cache(const df11_cache *c, const df11_cache_attention_args *p, Args &a)
     a.scale2 = (float)(p->scale * 1.44269504088896340736);
     if (!(a.scale2 > 0.0f && a.scale2 < INFINITY)) return df11::fail(DF11_E_ARG, "%s: scale must be positive", who);
     plan(a, true);
+    if (a.rows) {
+        const uintptr_t q = (uintptr_t)p->q, out = (uintptr_t)p->out;
+        const uintptr_t q_bytes = 2 * ((a.batch - 1) * a.q_batch + (a.tokens - 1) * a.q_token + (a.heads - 1) * a.q_head + a.dim);
+        a.out_on_q = out < q + q_bytes && q < out + 2 * (uintptr_t)(a.rows * a.dim);
+    }
     a.logit_stride = a.big ? 0 : (c->slots + 31) / 32 * 32;   // many rows: taken again, not kept
     return DF11_OK;
 }

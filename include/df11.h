@@ -479,7 +479,7 @@ typedef struct df11_prefix_attention_args {
     const void *q, *prefix_k, *prefix_v, *k, *v;
     const int32_t *lengths;       /* [batch] */
     const int32_t *block_table;   /* [batch, suffix / page], or NULL */
-    void *out;                    /* [batch, tokens, heads, dim], contiguous, the type of q */
+    void *out;                    /* [batch, tokens, heads, dim], contiguous, the type of q; may be q itself */
     float *lse;                   /* [batch, tokens, heads] natural log of the sum, or NULL */
     int64_t dtype, batch, tokens, heads, kv_heads, dim, prefix, suffix, page, n_pages;
     int64_t q_batch, q_token, q_head, prefix_token, prefix_head, k_batch, k_token, k_head, table_batch;
@@ -525,7 +525,7 @@ typedef struct df11_cache {
 typedef struct df11_cache_attention_args {
     const void *q;
     const int32_t *pos;           /* [batch] */
-    void *out;                    /* [batch, tokens, heads, dim], contiguous */
+    void *out;                    /* [batch, tokens, heads, dim], contiguous; may be q itself */
     int64_t tokens, heads, q_batch, q_token, q_head;
     double scale;
 } df11_cache_attention_args;

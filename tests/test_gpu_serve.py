@@ -808,3 +808,21 @@ def test_cache_attention_window_from_before_the_first_position(first):
     want, want_w, bound = ref.cache_attention(q, pos=pos, **clean)
     _close(out[:, at < 5], want[:, at < 5], bound[:, at < 5], "tokens before the value")
     _close(c.weights, want_w, 2.0 ** -12 * (want_w - x["weights"].double()) + 2.0 ** -22 * want_w, "weights")
+
+
+@pytest.mark.parametrize("T", [1, 40, 400])
+def test_attention_in_the_place_of_its_queries(T):
+    """out=q, few rows and many (whose weights are taken from q once more):
+    the same bits as into another tensor."""
+    x = _cache_case(3, 2, 2, 300, 128, [300, 290], more=9)
+    pos = torch.tensor([250, 260], dtype=torch.int32).cuda()
+    q = _randn(_gen(1), 2, T, 4, 128).cuda()
+    a, b = _cuda_cache(x), _cuda_cache(x)
+    out = serve.cache_attention(q, a, pos)
+    same = q.clone()
+    assert serve.cache_attention(same, b, pos, out=same).data_ptr() == same.data_ptr()
+    assert torch.equal(out, same) and torch.equal(a.weights, b.weights)
+    y = {n: t.cuda() if t is not None else None for n, t in _prefix_case(2, 2, T, 99, [T, T + 4], 4, 2, 128, BF).items()}
+    out = serve.prefix_attention(y["q"], y["pk"], y["pv"], y["k"], y["v"], y["lengths"])
+    serve.prefix_attention(y["q"], y["pk"], y["pv"], y["k"], y["v"], y["lengths"], out=y["q"])
+    assert torch.equal(out, y["q"])
