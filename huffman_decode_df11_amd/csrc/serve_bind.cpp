@@ -162,13 +162,6 @@ int64_t whole(PyObject *o)
 
 double scale_of(PyObject *o, int64_t dim) { return o == Py_None ? 1.0 / std::sqrt((double)(dim ? dim : 1)) : number(o); }
 
-// The cache that serve.py's BoundedCache keeps as bytes.
-const df11_cache &cache_of(PyObject *o)
-{
-    if (!PyBytes_Check(o) || PyBytes_GET_SIZE(o) != (Py_ssize_t)sizeof(df11_cache)) wrong_type("not a BoundedCache");
-    return *(const df11_cache *)PyBytes_AS_STRING(o);
-}
-
 PyObject *both(const at::Tensor &a, const at::Tensor &b)
 {
     PyObject *x = THPVariable_Wrap(a), *y = THPVariable_Wrap(b);
@@ -244,19 +237,34 @@ df11_cache make_cache(const at::Tensor &k, const at::Tensor &v, const at::Tensor
     return c;
 }
 
-PyObject *bytes_of(const df11_cache &c) { return PyBytes_FromStringAndSize((const char *)&c, sizeof c); }
+// The cache of a tuple (k, v, weights, positions, lengths), which serve.py's
+// BoundedCache keeps: the tensors are looked at in every call, since their
+// memory may have moved since the last one.
+df11_cache cache_of(PyObject *o)
+{
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 5) wrong_type("not a BoundedCache");
+    const auto at = [&](int i, const char *name) -> const at::Tensor & { return tensor(PyTuple_GET_ITEM(o, i), name); };
+    return make_cache(at(0, "k"), at(1, "v"), at(2, "weights"), at(3, "positions"), at(4, "lengths"));
+}
 
-// k, v, weights, positions, lengths
+// k, v, weights, positions, lengths: the tuple of them, looked over
 PyObject *cache(Arguments x)
 {
-    return bytes_of(make_cache(tensor(x[0], "k"), tensor(x[1], "v"), tensor(x[2], "weights"), tensor(x[3], "positions"),
-                               tensor(x[4], "lengths")));
+    PyObject *r = PyTuple_Pack(5, x[0], x[1], x[2], x[3], x[4]);
+    if (!r) return nullptr;
+    try {
+        cache_of(r);
+    } catch (...) {
+        Py_DECREF(r);
+        throw;
+    }
+    return r;
 }
 
 // cache, its k, q, pos, scale, out, stream
 PyObject *cache_attention(Arguments x)
 {
-    const df11_cache &c = cache_of(x[0]);
+    const df11_cache c = cache_of(x[0]);
     const at::Tensor &k = tensor(x[1], "k"), &q = tensor(x[2], "q"), &pos = tensor(x[3], "pos");
     const auto type = k.scalar_type();
     const auto device = k.device();
@@ -280,7 +288,7 @@ PyObject *cache_attention(Arguments x)
 // cache, its k, k_new, v_new, pos, recent, stream
 PyObject *cache_insert(Arguments x)
 {
-    const df11_cache &c = cache_of(x[0]);
+    const df11_cache c = cache_of(x[0]);
     const at::Tensor &k = tensor(x[1], "k"), &k_new = tensor(x[2], "k_new"), &v_new = tensor(x[3], "v_new");
     const at::Tensor &pos = tensor(x[4], "pos");
     const auto device = k.device();
@@ -294,10 +302,10 @@ PyObject *cache_insert(Arguments x)
 }
 
 // cache, its k, pos, budget, recent, slots, stream: the new cache's k, v,
-// weights, positions, lengths and bytes, and kept
+// weights, positions and lengths, and kept
 PyObject *cache_compact(Arguments x)
 {
-    const df11_cache &c = cache_of(x[0]);
+    const df11_cache c = cache_of(x[0]);
     const at::Tensor &k = tensor(x[1], "k"), &pos = tensor(x[2], "pos");
     const int64_t budget = whole(x[3]), recent = whole(x[4]), slots = whole(x[5]);
     if (slots < 1) wrong_value("the new cache needs a slot");
@@ -311,12 +319,10 @@ PyObject *cache_compact(Arguments x)
     check(lib.compact(&c, p, budget, recent, &out, (int32_t *)kept.data_ptr(), (int32_t *)lengths.data_ptr(),
                       (void *)whole(x[6])),
           "df11_cache_compact");
-    PyObject *r = PyTuple_New(7);
+    PyObject *r = PyTuple_New(6);
     if (!r) return nullptr;
-    const at::Tensor *parts[5] = {&k2, &v2, &weights, &positions, &lengths};
-    for (int i = 0; i < 5; i++) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(*parts[i]));
-    PyTuple_SET_ITEM(r, 5, bytes_of(out));
-    PyTuple_SET_ITEM(r, 6, THPVariable_Wrap(kept));
+    const at::Tensor *parts[6] = {&k2, &v2, &weights, &positions, &lengths, &kept};
+    for (int i = 0; i < 6; i++) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(*parts[i]));
     return r;
 }
 

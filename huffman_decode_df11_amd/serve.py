@@ -101,11 +101,10 @@ class BoundedCache:
     NO_TOKEN hold none; slots at or past a sequence's next position (refused
     drafts) are not seen and are replaced first."""
 
-    def __init__(self, k, v, weights, positions, lengths, args: Optional[bytes] = None):
-        if args is None:
-            args = _native.cache(k, v, weights, positions, lengths)
-        # args: the df11_cache struct, checked once
-        self.__dict__.update(k=k, v=v, weights=weights, positions=positions, lengths=lengths, args=args)
+    def __init__(self, k, v, weights, positions, lengths):
+        # args: the tensors as the binding takes them, which reads their addresses and checks them in every call
+        self.__dict__.update(k=k, v=v, weights=weights, positions=positions, lengths=lengths,
+                             args=_native.cache(k, v, weights, positions, lengths))
 
     def __setattr__(self, name, value):
         raise AttributeError("a BoundedCache keeps its tensors: write into %s, or make another cache" % name)

@@ -2,6 +2,9 @@
 (serve_reference.py): types, head layouts, lengths from none to several
 workgroups' ranges, page sizes, strides, masked places that hold NaN and
 infinities, rows that see nothing, streams and graphs."""
+import copy
+import pickle
+
 import numpy as np
 import pytest
 
@@ -826,3 +829,40 @@ def test_attention_in_the_place_of_its_queries(T):
     out = serve.prefix_attention(y["q"], y["pk"], y["pv"], y["k"], y["v"], y["lengths"])
     serve.prefix_attention(y["q"], y["pk"], y["pv"], y["k"], y["v"], y["lengths"], out=y["q"])
     assert torch.equal(out, y["q"])
+
+
+@pytest.mark.parametrize("how", ["copied", "pickled"])
+def test_a_copy_of_a_cache_has_its_own_memory(how):
+    a = _cuda_cache(_cache_case(4, 2, 2, 20, 64, [20, 11]))
+    b = copy.deepcopy(a) if how == "copied" else pickle.loads(pickle.dumps(a))
+    names = ("k", "v", "weights", "positions", "lengths")
+    before = [getattr(a, n).clone() for n in names]
+    row, pos = _randn(_gen(1), 2, 2, 64).cuda(), torch.tensor([30, 31], dtype=torch.int32, device="cuda")
+    slots, _ = serve.cache_insert(b, row, row, pos, 2)
+    serve.cache_attention(row[:, None], b, pos)
+    for n, t in zip(names, before):
+        assert torch.equal(getattr(a, n), t), n
+    for i in range(2):
+        for h in range(2):
+            assert torch.equal(b.k[i, h, int(slots[i, h])], row[i, h]) and int(b.positions[i, h, int(slots[i, h])]) == 30 + i
+    assert bool((b.weights != before[2]).any())
+
+
+def test_a_cache_whose_tensors_get_other_memory():
+    """set_, resize_: the next call uses the memory there is, or refuses its shape."""
+    x = _cache_case(5, 2, 2, 40, 64, [40, 33])
+    a, b = _cuda_cache(x), _cuda_cache(x)
+    held = [getattr(a, n).untyped_storage() for n in ("k", "v", "weights", "positions")]
+    for n in ("k", "v", "weights", "positions"):
+        t = getattr(a, n)
+        t.set_(t.clone())
+    old = torch.empty(0, device="cuda").set_(held[2], 0, (2, 2, 40), (80, 40, 1)).clone()
+    q, pos = _randn(_gen(1), 2, 1, 4, 64).cuda(), torch.tensor([35, 31], dtype=torch.int32, device="cuda")
+    assert torch.equal(serve.cache_attention(q, a, pos), serve.cache_attention(q, b, pos))
+    assert torch.equal(a.weights, b.weights) and bool((a.weights != x["weights"].cuda()).any())
+    assert torch.equal(torch.empty(0, device="cuda").set_(held[2], 0, (2, 2, 40), (80, 40, 1)), old)
+    a.k.resize_(2, 2, 20, 64)
+    for call in (lambda: serve.cache_attention(q, a, pos), lambda: serve.cache_compact(a, pos, 4, 1),
+                 lambda: serve.cache_insert(a, q[:, 0, :2], q[:, 0, :2], pos, 1)):
+        with pytest.raises(ValueError):
+            call()
