@@ -12,6 +12,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/core/LegacyTypeDispatch.h>
+#include <ATen/core/grad_mode.h>
 #include <torch/csrc/Exceptions.h>
 
 #include <cmath>
@@ -70,6 +71,8 @@ void same(const char *name, const at::Tensor &t, at::ScalarType type, at::Device
         wrong_type(std::string(name) + " must be " + c10::toString(type) + ", got " + c10::toString(t.scalar_type()));
     if (t.device() != device)
         wrong_value(std::string(name) + " is on " + t.device().str() + ", the other operands on " + device.str());
+    if (t.requires_grad() && at::GradMode::is_enabled())
+        wrong_value(std::string(name) + " requires a gradient, which these operators do not give: call them under torch.no_grad()");
     if (t.sizes() != shape)
         wrong_value(std::string(name) + " has shape " + text(t.sizes()) + ", not " + text(shape));
 }

@@ -17,7 +17,9 @@ the library are native (csrc/serve_bind.cpp); there is no fallback
 implementation.  Work is enqueued on ``stream`` (the device's current stream
 when None); outputs and workspaces are allocated on it.  A tensor of the
 wrong type raises TypeError, one of the wrong shape, device or strides
-ValueError, what the library refuses DF11Error.
+ValueError, what the library refuses DF11Error.  There are no gradients: a
+tensor that requires one raises ValueError unless gradients are off
+(torch.no_grad, torch.inference_mode).
 """
 from __future__ import annotations
 

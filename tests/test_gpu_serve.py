@@ -866,3 +866,35 @@ def test_a_cache_whose_tensors_get_other_memory():
                  lambda: serve.cache_insert(a, q[:, 0, :2], q[:, 0, :2], pos, 1)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_gradients_are_refused():
+    """Each floating operand that requires a gradient, unless gradients are off."""
+    x = {n: t.cuda() if t is not None else None for n, t in _prefix_case(1, 2, 1, 9, [3, 4], 4, 2, 64, BF).items()}
+    y = _cache_case(6, 2, 2, 20, 64, [20, 20])
+    cache, pos = _cuda_cache(y), torch.tensor([30, 30], dtype=torch.int32, device="cuda")
+    q, row = _randn(_gen(2), 2, 1, 4, 64).cuda(), _randn(_gen(3), 2, 2, 64).cuda()
+    tokens, target, uniforms = torch.zeros(2, 3, dtype=torch.int64, device="cuda"), torch.rand(2, 4, 50, device="cuda"), \
+        torch.rand(2, 4, device="cuda")
+    draft = target[:, :3].clone()
+    calls = [(serve.prefix_attention, [x[n] for n in ("q", "pk", "pv", "k", "v", "lengths")], range(5)),
+             (serve.cache_attention, [q, cache, pos], [0]),
+             (serve.cache_insert, [cache, row, row.clone(), pos, 2], [1, 2]),
+             (serve.verify_drafts, [tokens, target, uniforms, draft], [1, 2, 3]),
+             (serve.BoundedCache, [y[n].cuda() for n in ("k", "v", "weights", "positions", "lengths")], range(3))]
+    for call, args, floats in calls:
+        call(*args)
+        for i in floats:
+            some = list(args)
+            some[i] = args[i].clone().requires_grad_()
+            with pytest.raises(ValueError, match="gradient"):
+                call(*some)
+            with torch.no_grad():
+                call(*some)
+    held = _cuda_cache(y)
+    held.k.requires_grad_()
+    for call in (lambda: serve.cache_attention(q, held, pos), lambda: serve.cache_compact(held, pos, 4, 1)):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        with torch.inference_mode():
+            call()
