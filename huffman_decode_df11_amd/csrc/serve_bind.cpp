@@ -139,6 +139,13 @@ at::Tensor make(at::IntArrayRef shape, const at::Tensor &like, at::ScalarType ty
     return at::empty(shape, like.options().dtype(type));
 }
 
+// A tensor that a call has written in place: its version counts that, so that
+// what autograd saved of it is known to have changed.
+void written(const at::Tensor &t)
+{
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 struct Workspace {
     at::Tensor t;
     uint64_t bytes;
@@ -220,6 +227,7 @@ PyObject *prefix_attention(Arguments x)
     a.scale = scale_of(x[7], a.dim);
     Workspace ws(lib.prefix_bytes(&a), q);
     check(lib.prefix(&a, ws.data(), ws.bytes, (void *)whole(x[10])), "df11_prefix_attention");
+    if (x[8] != Py_None) written(out);
     return return_lse ? both(out, lse) : THPVariable_Wrap(out);
 }
 
@@ -248,6 +256,12 @@ df11_cache cache_of(PyObject *o)
     if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 5) wrong_type("not a BoundedCache");
     const auto at = [&](int i, const char *name) -> const at::Tensor & { return tensor(PyTuple_GET_ITEM(o, i), name); };
     return make_cache(at(0, "k"), at(1, "v"), at(2, "weights"), at(3, "positions"), at(4, "lengths"));
+}
+
+// `n` tensors of such a tuple, from `first` on, were written.
+void written(PyObject *cache, int first, int n)
+{
+    for (int i = first; i < first + n; i++) written(THPVariable_Unpack(PyTuple_GET_ITEM(cache, i)));
 }
 
 // k, v, weights, positions, lengths: the tuple of them, looked over
@@ -285,6 +299,8 @@ PyObject *cache_attention(Arguments x)
     a.scale = scale_of(x[4], c.dim);
     Workspace ws(lib.attend_bytes(&c, &a), q);
     check(lib.attend(&c, &a, ws.data(), ws.bytes, (void *)whole(x[6])), "df11_cache_attention");
+    if (x[5] != Py_None) written(out);
+    written(x[0], 2, 1);   // weights
     return THPVariable_Wrap(out);
 }
 
@@ -301,6 +317,7 @@ PyObject *cache_insert(Arguments x)
     check(lib.insert(&c, k_new.data_ptr(), v_new.data_ptr(), s.s[0], s.s[1], p, whole(x[5]), (int32_t *)slots.data_ptr(),
                      (int32_t *)lengths.data_ptr(), (void *)whole(x[6])),
           "df11_cache_insert");
+    written(x[0], 0, 4);   // k, v, weights, positions
     return both(slots, lengths);
 }
 

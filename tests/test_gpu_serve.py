@@ -898,3 +898,29 @@ def test_gradients_are_refused():
             call()
         with torch.inference_mode():
             call()
+
+
+def test_writes_in_place_are_counted():
+    """The versions of what a call writes grow, those of what it reads do not; inference tensors have none."""
+    c = _cuda_cache(_cache_case(7, 1, 2, 20, 64, [20]))
+    names = ("k", "v", "weights", "positions", "lengths")
+    version = lambda: [getattr(c, n)._version for n in names]   # noqa: E731
+    row, q = _randn(_gen(1), 1, 2, 64).cuda(), _randn(_gen(2), 1, 1, 4, 64).cuda()
+    pos, out = torch.tensor([30], dtype=torch.int32, device="cuda"), torch.empty(1, 1, 4, 64, dtype=BF, device="cuda")
+    old = version()
+    serve.cache_insert(c, row, row, pos, 2)
+    assert [new > o for new, o in zip(version(), old)] == [True, True, True, True, False]
+    old, old_out = version(), out._version
+    serve.cache_attention(q, c, pos, out=out)
+    assert [new > o for new, o in zip(version(), old)] == [False, False, True, False, False] and out._version > old_out
+    old = version()
+    serve.cache_compact(c, pos, 5, 1)
+    assert version() == old and q._version == row._version == pos._version == 0
+    old_out = out._version
+    serve.prefix_attention(q, row.transpose(0, 1).expand(2, 2, 64).contiguous(), row.transpose(0, 1).expand(2, 2, 64).contiguous(),
+                           row[:, None], row[:, None], pos, out=out)
+    assert out._version > old_out
+    with torch.inference_mode():
+        other = _cuda_cache(_cache_case(7, 1, 2, 20, 64, [20]))
+    serve.cache_insert(other, row, row, pos, 2)
+    serve.cache_attention(q, other, pos)
