@@ -170,6 +170,13 @@ int64_t whole(PyObject *o)
     return x;
 }
 
+bool truth(PyObject *o)
+{
+    const int x = PyObject_IsTrue(o);
+    if (x < 0) throw Status{};
+    return x;
+}
+
 double scale_of(PyObject *o, int64_t dim) { return o == Py_None ? 1.0 / std::sqrt((double)(dim ? dim : 1)) : number(o); }
 
 PyObject *both(const at::Tensor &a, const at::Tensor &b)
@@ -215,7 +222,7 @@ PyObject *prefix_attention(Arguments x)
     if (x[8] == Py_None) out = make(q.sizes(), q, type);
     else out = tensor(x[8], "out");
     a.out = flat("out", out, type, device, q.sizes());
-    const bool return_lse = x[9] == Py_True;
+    const bool return_lse = truth(x[9]);
     at::Tensor lse;
     if (return_lse) {
         lse = make({a.batch, a.tokens, a.heads}, q, at::kFloat);

@@ -924,3 +924,14 @@ def test_writes_in_place_are_counted():
         other = _cuda_cache(_cache_case(7, 1, 2, 20, 64, [20]))
     serve.cache_insert(other, row, row, pos, 2)
     serve.cache_attention(q, other, pos)
+
+
+@pytest.mark.parametrize("yes,no", [(True, False), (1, 0), (np.bool_(True), np.bool_(False)), ("yes", None)])
+def test_return_lse_is_any_truth_value(yes, no):
+    x = {n: t.cuda() if t is not None else None for n, t in _prefix_case(1, 2, 1, 9, [3, 4], 4, 2, 64, BF).items()}
+    args = [x[n] for n in ("q", "pk", "pv", "k", "v", "lengths")]
+    out, lse = serve.prefix_attention(*args, return_lse=yes)
+    assert lse.shape == (2, 1, 4)
+    assert torch.equal(serve.prefix_attention(*args, return_lse=no), out)
+    with pytest.raises(ValueError):   # an array of two has no truth value
+        serve.prefix_attention(*args, return_lse=np.array([True, False]))
