@@ -284,6 +284,24 @@ int make_cache(const char *who, const df11_cache *c, bool lengths, Cache &a)
     return DF11_OK;
 }
 
+// Whether no two slots' rows share memory, as those of a cache that is
+// written must not (workgroups of different heads would race): each axis has
+// to step over all that the axes of smaller strides span.
+bool rows_apart(const df11_cache *c)
+{
+    struct Axis {
+        int64_t stride, size;
+    } axes[3] = {{c->stride_batch, c->batch}, {c->stride_head, c->kv_heads}, {c->stride_slot, c->slots}};
+    std::sort(axes, axes + 3, [](const Axis &x, const Axis &y) { return x.stride < y.stride; });
+    __int128 span = c->dim;
+    for (const Axis &axis : axes) {
+        if (axis.size <= 1) continue;
+        if (axis.stride < span) return false;
+        span += (__int128)axis.stride * (axis.size - 1);
+    }
+    return true;
+}
+
 int launched(const char *who)
 {
     const hipError_t e = hipGetLastError();
@@ -307,6 +325,7 @@ extern "C" int df11_cache_insert(const df11_cache *cache, const void *k_new, con
     if (new_batch < 0 || new_head < 0 || (new_batch | new_head) % 8)
         return df11::fail(DF11_E_ARG, "%s: strides must be multiples of 8", who);
     if (recent < 0) return df11::fail(DF11_E_ARG, "%s: recent is negative", who);
+    if (!rows_apart(cache)) return df11::fail(DF11_E_ARG, "%s: slots of the cache share memory", who);
     hipLaunchKernelGGL(insert_kernel, dim3(c.batch * c.kv_heads), dim3(kInsertThreads), 0, (hipStream_t)stream, c,
                        (const uint16_t *)k_new, (const uint16_t *)v_new, new_batch, new_head, pos,
                        std::min<int64_t>(recent, 1ll << 32), out_slots, out_lengths);
@@ -329,6 +348,7 @@ extern "C" int df11_cache_compact(const df11_cache *cache, const int32_t *pos, i
     if (!c.batch) return DF11_OK;
     if (!pos || !kept || !out_lengths || out_lengths == c.lengths)
         return df11::fail(DF11_E_ARG, "%s: null or shared pointer", who);
+    if (!rows_apart(out_cache)) return df11::fail(DF11_E_ARG, "%s: slots of the new cache share memory", who);
     if (c.slots && (out.k == c.k || out.v == c.v || out.weights == c.weights || out.positions == c.positions))
         return df11::fail(DF11_E_ARG, "%s: a cache is not cut down in place", who);
     hipStream_t st = (hipStream_t)stream;

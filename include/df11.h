@@ -546,7 +546,8 @@ int df11_cache_attention(const df11_cache *c, const df11_cache_attention_args *a
  * ones that are left keep their positions (df11_cache above).  out_slots [batch, kv_heads]: the slot taken, or
  * -1.  out_lengths [batch]: min(lengths[b] + 1, slots), lengths[b] for a
  * sequence that takes none (lengths itself is not written; out_lengths must
- * be another array).  Errors: as df11_prefix_attention. */
+ * be another array).  Errors: as df11_prefix_attention, and E_ARG for a cache
+ * whose slots share memory (a stride smaller than what lies inside it). */
 int df11_cache_insert(const df11_cache *c, const void *k_new, const void *v_new, int64_t new_batch,
                       int64_t new_head, const int32_t *pos, int64_t recent, int32_t *out_slots,
                       int32_t *out_lengths, void *stream);
@@ -560,7 +561,7 @@ int df11_cache_insert(const df11_cache *c, const void *k_new, const void *v_new,
  * slots of `c` that were kept, -1 behind them.  Slots of `out` behind the
  * kept ones are zero with weight 0 and position DF11_NO_TOKEN.  out_lengths[b] =
  * min(lengths[b], budget).  Errors: as df11_prefix_attention, and E_ARG for
- * recent > budget or budget > out->slots. */
+ * recent > budget, budget > out->slots or an `out` whose slots share memory. */
 int df11_cache_compact(const df11_cache *c, const int32_t *pos, int64_t budget, int64_t recent,
                        const df11_cache *out, int32_t *kept, int32_t *out_lengths, void *stream);
 

@@ -935,3 +935,34 @@ def test_return_lse_is_any_truth_value(yes, no):
     assert torch.equal(serve.prefix_attention(*args, return_lse=no), out)
     with pytest.raises(ValueError):   # an array of two has no truth value
         serve.prefix_attention(*args, return_lse=np.array([True, False]))
+
+
+def test_expanded_caches_are_read_and_not_written():
+    """Heads that share one key tensor: attention and compaction as of a cache
+    of copies, insertion refused; head-last and interleaved caches are written."""
+    x = _cache_case(8, 2, 1, 30, 64, [30, 25])
+    c = {n: t.cuda() for n, t in x.items()}
+    both = {n: c[n].expand(2, 4, 30).contiguous() for n in ("weights", "positions")}
+    shared = serve.BoundedCache(c["k"].expand(2, 4, 30, 64), c["v"].expand(2, 4, 30, 64), both["weights"], both["positions"],
+                                c["lengths"])
+    copies = serve.BoundedCache(c["k"].repeat(1, 4, 1, 1), c["v"].repeat(1, 4, 1, 1), both["weights"].clone(),
+                                both["positions"], c["lengths"])
+    q, pos = _randn(_gen(1), 2, 1, 8, 64).cuda(), torch.tensor([28, 29], dtype=torch.int32, device="cuda")
+    assert torch.equal(serve.cache_attention(q, shared, pos), serve.cache_attention(q, copies, pos))
+    assert torch.equal(shared.weights, copies.weights)
+    a, b = serve.cache_compact(shared, pos, 9, 2), serve.cache_compact(copies, pos, 9, 2)
+    assert torch.equal(a[1], b[1]) and torch.equal(a[0].k, b[0].k)
+    row = _randn(_gen(2), 2, 4, 64).cuda()
+    before = c["k"].clone()
+    with pytest.raises(RuntimeError, match="share memory"):
+        serve.cache_insert(shared, row, row, pos, 2)
+    assert torch.equal(c["k"], before)
+    slots, _ = serve.cache_insert(copies, row, row, pos, 2)
+    for layout in ("slots before heads", "keys beside values"):
+        if layout == "slots before heads":
+            k, v = (t.repeat(1, 4, 1, 1).transpose(1, 2).contiguous().transpose(1, 2) for t in (c["k"], c["v"]))
+        else:
+            k, v = torch.stack([c["k"].repeat(1, 4, 1, 1), c["v"].repeat(1, 4, 1, 1)], 3).unbind(3)
+        other = serve.BoundedCache(k, v, shared.weights.clone(), c["positions"].expand(2, 4, 30).contiguous(), c["lengths"])
+        got, _ = serve.cache_insert(other, row, row, pos, 2)
+        assert torch.equal(got, slots) and torch.equal(other.k, copies.k) and torch.equal(other.v, copies.v)

@@ -172,3 +172,13 @@ def test_binding_refuses_what_is_not_on_the_gpu():
         native.cache_attention(b"", k, q, n, None, None, 0)
     with pytest.raises(TypeError, match="arguments"):
         native.verify_drafts(n)
+
+
+@pytest.mark.parametrize("change", [dict(stride_head=0), dict(stride_batch=0), dict(stride_slot=0), dict(stride_slot=56),
+                                    dict(stride_head=2552), dict(stride_batch=2560), dict(stride_batch=64)])
+def test_caches_whose_slots_share_memory_are_not_written(change):
+    L = _lib.lib()
+    assert L.df11_cache_insert(ctypes.byref(_cache(**change)), PTR, PTR, 128, 64, PTR, 1, PTR, PTR + 64, None) == ARG
+    out = _cache(k=PTR + 64, v=PTR + 64, weights=PTR + 64, positions=PTR + 64, **change)
+    assert L.df11_cache_compact(ctypes.byref(_cache()), PTR, 4, 1, ctypes.byref(out), PTR, PTR + 64, None) == ARG
+    assert b"share memory" in L.df11_last_error()
