@@ -302,6 +302,31 @@ bool rows_apart(const df11_cache *c)
     return true;
 }
 
+bool meet(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes)
+{
+    return (uintptr_t)a < (uintptr_t)b + b_bytes && (uintptr_t)b < (uintptr_t)a + a_bytes;
+}
+
+// Whether the new cache lies on the one it is cut out of: in weights or
+// positions, or in keys or values without gaps.  (Two caches may take turns
+// in one allocation: rows with gaps are the caller's to keep apart.)
+bool caches_meet(const df11_cache *c, const df11_cache *out)
+{
+    const auto slots = [](const df11_cache *x) { return x->batch * x->kv_heads * x->slots; };
+    if (!slots(c) || !slots(out)) return false;
+    if (meet(c->weights, 4 * slots(c), out->weights, 4 * slots(out)) ||
+        meet(c->positions, 4 * slots(c), out->positions, 4 * slots(out)))
+        return true;
+    const auto dense = [&](const df11_cache *x) {
+        return (x->batch - 1) * x->stride_batch + (x->kv_heads - 1) * x->stride_head + (x->slots - 1) * x->stride_slot +
+                   x->dim == slots(x) * x->dim;
+    };
+    const int64_t bytes = 2 * slots(c) * c->dim, out_bytes = 2 * slots(out) * out->dim;
+    return dense(c) && dense(out) &&
+           (meet(c->k, bytes, out->k, out_bytes) || meet(c->k, bytes, out->v, out_bytes) ||
+            meet(c->v, bytes, out->k, out_bytes) || meet(c->v, bytes, out->v, out_bytes));
+}
+
 int launched(const char *who)
 {
     const hipError_t e = hipGetLastError();
@@ -349,7 +374,7 @@ extern "C" int df11_cache_compact(const df11_cache *cache, const int32_t *pos, i
     if (!pos || !kept || !out_lengths || out_lengths == c.lengths)
         return df11::fail(DF11_E_ARG, "%s: null or shared pointer", who);
     if (!rows_apart(out_cache)) return df11::fail(DF11_E_ARG, "%s: slots of the new cache share memory", who);
-    if (c.slots && (out.k == c.k || out.v == c.v || out.weights == c.weights || out.positions == c.positions))
+    if (c.slots && (out.k == c.k || out.v == c.v || caches_meet(cache, out_cache)))
         return df11::fail(DF11_E_ARG, "%s: a cache is not cut down in place", who);
     hipStream_t st = (hipStream_t)stream;
     const auto select = [&](auto kernel) {

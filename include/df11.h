@@ -554,7 +554,7 @@ int df11_cache_insert(const df11_cache *c, const void *k_new, const void *v_new,
 
 /* A cache cut down to `budget` slots for each sequence and key head, into
  * another cache `out` (of out->slots >= budget slots, same batch, heads,
- * dim and type; out->lengths is not used).  With pos[b] the sequence's next
+ * dim and type; out->lengths is not used; no memory shared with `c`).  With pos[b] the sequence's next
  * position: stale slots are dropped; of the others the `recent` latest
  * positions are kept, then the greatest weights, the lowest slot of equals
  * (NaN as above), `budget` in all; they keep their slot order.  kept [batch, kv_heads, out->slots]: the

@@ -966,3 +966,34 @@ def test_expanded_caches_are_read_and_not_written():
         other = serve.BoundedCache(k, v, shared.weights.clone(), c["positions"].expand(2, 4, 30).contiguous(), c["lengths"])
         got, _ = serve.cache_insert(other, row, row, pos, 2)
         assert torch.equal(got, slots) and torch.equal(other.k, copies.k) and torch.equal(other.v, copies.v)
+
+
+def test_cache_compact_within_one_allocation():
+    """Old and new slots behind each other in one allocation's rows."""
+    import ctypes
+
+    from huffman_decode_df11_amd import _lib
+    B, H, C, N, D = 2, 2, 50, 20, 64
+    x = _cache_case(9, B, H, C, D, [50, 41], more=5)
+    pool = torch.zeros(2, B, H, C + N, D, dtype=BF, device="cuda")
+    pool[0, :, :, :C], pool[1, :, :, :C] = x["k"].cuda(), x["v"].cuda()
+    arrays = {n: x[n].cuda() for n in ("weights", "positions", "lengths")}
+    new_weights, new_positions = torch.empty(B, H, N, device="cuda"), torch.empty(B, H, N, dtype=torch.int32, device="cuda")
+    kept, new_lengths = torch.empty(B, H, N, dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+    pos = torch.tensor([55, 50], dtype=torch.int32, device="cuda")
+
+    def struct(first, slots, weights, positions):
+        return _lib.Cache(k=pool[0, :, :, first:].data_ptr(), v=pool[1, :, :, first:].data_ptr(), weights=weights.data_ptr(),
+                          positions=positions.data_ptr(), lengths=arrays["lengths"].data_ptr(), dtype=_lib.DF11_BF16, batch=B,
+                          kv_heads=H, slots=slots, dim=D, stride_batch=H * (C + N) * D, stride_head=(C + N) * D, stride_slot=D)
+
+    old, new = struct(0, C, arrays["weights"], arrays["positions"]), struct(C, N, new_weights, new_positions)
+    _lib.check(_lib.lib().df11_cache_compact(ctypes.byref(old), pos.data_ptr(), N, 4, ctypes.byref(new), kept.data_ptr(),
+                                             new_lengths.data_ptr(), torch.cuda.current_stream().cuda_stream), "compact")
+    want = ref.cache_compact(x["positions"], x["weights"], x["lengths"], pos.cpu(), N, 4)
+    assert torch.equal(kept.cpu(), want)
+    at = want.clamp(min=0).long()
+    rows = at.unsqueeze(-1).expand(B, H, N, D)
+    for i, n in enumerate(("k", "v")):
+        assert torch.equal(pool[i, :, :, :C].cpu(), x[n])
+        assert torch.equal(pool[i, :, :, C:].cpu(), torch.where((want >= 0).unsqueeze(-1), x[n].gather(2, rows), 0))

@@ -182,3 +182,17 @@ def test_caches_whose_slots_share_memory_are_not_written(change):
     out = _cache(k=PTR + 64, v=PTR + 64, weights=PTR + 64, positions=PTR + 64, **change)
     assert L.df11_cache_compact(ctypes.byref(_cache()), PTR, 4, 1, ctypes.byref(out), PTR, PTR + 64, None) == ARG
     assert b"share memory" in L.df11_last_error()
+
+
+@pytest.mark.parametrize("change", [dict(k=PTR + 64), dict(v=PTR + 64), dict(k=PTR + (1 << 20) - 64), dict(weights=PTR + 16),
+                                    dict(positions=PTR + (1 << 20) + 48), dict(weights=PTR - 64)])
+def test_caches_that_lie_on_each_other_are_not_cut_down(change):
+    """Each part of the new cache that begins inside the old one, or ends in it."""
+    far = 1 << 20   # nothing here is followed: the old cache holds 2 * 2 * 40 slots of 64 dims
+    old = _cache(v=PTR + far, positions=PTR + far)
+    apart = dict(slots=10, k=PTR + 2 * far, v=PTR + 3 * far, weights=PTR + 2 * far, positions=PTR + 3 * far,
+                 stride_batch=1280, stride_head=640)
+    L = _lib.lib()
+    out = _cache(**{**apart, **change})
+    assert L.df11_cache_compact(ctypes.byref(old), PTR, 4, 1, ctypes.byref(out), PTR, PTR + 64, None) == ARG
+    assert b"in place" in L.df11_last_error()
