@@ -113,6 +113,8 @@ class Generator:
     def __init__(self, model: Decoder, prompt, batch: int, budget: int = 256, recent: int = 32, drafts: int = 4,
                  room: int = 512, page: int = 16, temperature: float = 1.0, seed: int = 0):
         c, device = model.config, model.device
+        if not prompt.numel():
+            raise ValueError("the prompt needs a token")
         self.model, self.batch, self.recent, self.drafts, self.temperature = model, batch, recent, drafts, temperature
         self.random = torch.Generator(device=device).manual_seed(seed)
         pages = -(-(room + drafts + 1) // page)
@@ -146,6 +148,9 @@ class Generator:
             model(prompt[None, at:at + n].to(model.device), torch.arange(at, at + n, device=model.device)[None], attend)
         self.caches: List[serve.BoundedCache] = []
         for i in range(c.layers):
+            if not P:   # a prompt of one token: nothing to keep yet
+                self.caches.append(serve.BoundedCache.empty(self.batch, c.kv_heads, budget, c.dim, device=model.device))
+                continue
             q = window[i][:, -self.WINDOW:]
             place = torch.arange(P, dtype=torch.int32, device=model.device).expand(1, c.kv_heads, P).contiguous()
             whole = serve.BoundedCache(kv[i][0][None].transpose(1, 2), kv[i][1][None].transpose(1, 2),

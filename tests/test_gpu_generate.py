@@ -106,3 +106,16 @@ def test_refused_drafts_leave_the_bounded_caches(prompt, budget, drafts, seed, m
                     there = [p for p in there if p != serve.NO_TOKEN]
                     assert len(there) == len(set(there)) and max(there) < int(nxt[b])
     assert refused > 40
+
+
+def test_prompt_of_one_token():
+    """Nothing before the sequences' own positions: greedy tokens are the full model's (the bound above)."""
+    model = generate.Decoder(generate.Config(vocab=1024), seed=3)
+    prompt = torch.tensor([17])
+    out, _ = generate.Generator(model, prompt, batch=2, budget=24, recent=8, drafts=3, room=64, temperature=0.0).generate(30)
+    assert out[0] == out[1] and len(out[0]) == 30
+    logits = _reference_logits(model, torch.cat([prompt, torch.tensor(out[0])])[:-1])
+    short = logits.max(1).values - logits.gather(1, torch.tensor(out[0])[:, None])[:, 0]
+    assert float(short.max()) < 0.32, short
+    with pytest.raises(ValueError, match="prompt"):
+        generate.Generator(model, prompt[:0], batch=2)
