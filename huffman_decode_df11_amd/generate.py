@@ -104,7 +104,7 @@ class Decoder:
 class Generator:
     """A batch that continues one prompt.  budget, recent: the bounded
     cache's slots and the latest positions it always keeps; drafts: tokens
-    proposed at a time; room: positions a sequence may add; page: positions
+    proposed at a time (0: none, one token a round); room: positions a sequence may add; page: positions
     of a page of its own cache."""
 
     CHUNK = 256    # prompt tokens at a time
@@ -169,7 +169,9 @@ class Generator:
 
     def draft(self):
         """Tokens proposed over the bounded caches [B, drafts], and the
-        distributions they were drawn from."""
+        distributions they were drawn from (None without drafts)."""
+        if not self.drafts:
+            return self.last.new_zeros((self.batch, 0)), None
         tokens, probs, ids, at = [], [], self.last, self._positions()
         for g in range(self.drafts + 1):
             def attend(i, q, k, v):

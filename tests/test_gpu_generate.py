@@ -119,3 +119,14 @@ def test_prompt_of_one_token():
     assert float(short.max()) < 0.32, short
     with pytest.raises(ValueError, match="prompt"):
         generate.Generator(model, prompt[:0], batch=2)
+
+
+def test_without_drafts():
+    """One token a round, the full model's (the bound above)."""
+    model = generate.Decoder(generate.Config(vocab=1024), seed=3)
+    prompt = torch.randint(1024, (70,), generator=torch.Generator().manual_seed(4))
+    out, taken = generate.Generator(model, prompt, batch=2, budget=24, recent=8, drafts=0, room=20, temperature=0.0).generate(12)
+    assert taken == 0.0 and out[0] == out[1] and len(out[0]) == 12
+    logits = _reference_logits(model, torch.cat([prompt, torch.tensor(out[0])])[:-1])[69:]
+    short = logits.max(1).values - logits.gather(1, torch.tensor(out[0])[:, None])[:, 0]
+    assert float(short.max()) < 0.32, short
