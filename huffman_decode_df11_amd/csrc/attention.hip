@@ -14,7 +14,10 @@
 // rounded to the operands' type (to nearest) for the product with V, since
 // the matrix cores take both operands in one type; their sum is taken before
 // that, so lse and weights keep float32 accuracy, and the outputs' error is
-// 1.1 to 1.4 times that of their own rounding.
+// 1.1 to 1.4 times that of their own rounding.  A float16 probability keeps
+// its 11 bits down to 2^-21 of the row's greatest so far and is gone below 2^-32
+// (kLift; without it 2^-14 and 2^-25: 31 keys of 2^-24.6 beside one of 1 gave
+// half as much again as they should); a bfloat16 one keeps its 8 throughout.
 //
 // attend_wave: one wave, 16 rows, 32 keys at a time, no LDS.
 //   S^T = K Q^T  v_mfma_f32_16x16x32: the A operand of lane l is key l % 16,
@@ -292,12 +295,14 @@ __device__ __forceinline__ void attend_wave(const Src &src, const u32x4 (&q)[DP 
         }
         mx = fmaxf(mx, __shfl_xor(mx, 16));
         mx = fmaxf(mx, __shfl_xor(mx, 32));
-        // The running maximum is raised only past 2^8 times itself: a
-        // probability of up to 2^8 is no less exact, and the sums are seldom scaled.
-        const bool raise = mx > m + 8.0f;
+        // m is kLift below the running maximum, which is raised only past 2^8
+        // times itself: a probability of up to 2^(8 + kLift) is no less exact,
+        // and the sums are seldom scaled.
+        const float low = mx - E::kLift;
+        const bool raise = low > m + 8.0f;
         if (__any(raise)) {
-            const float f = raise ? exp2_fast(m - mx) : 1.0f;
-            m = raise ? mx : m;
+            const float f = raise ? exp2_fast(m - low) : 1.0f;
+            m = raise ? low : m;
             l *= f;
 #pragma unroll
             for (int j = 0; j < W; j++) o[j] *= f;
@@ -617,12 +622,11 @@ __device__ __forceinline__ void tile_block(const Args &a, char *lds, int seq, in
 #pragma unroll
             for (int r = 0; r < 16; r++) mx = fmaxf(mx, s[k][r]);
         mx = fmaxf(mx, __shfl_xor(mx, 32)) * a.scale2;
-        // The running maximum is raised only past 2^8 times itself: a
-        // probability of up to 2^8 is no less exact, and the sums are seldom scaled.
-        const bool raise = mx > m + 8.0f;
+        const float low = mx - E::kLift;   // as in attend_wave
+        const bool raise = low > m + 8.0f;
         if (__any(raise)) {
-            const float by = raise ? exp2_fast(m - mx) : 1.0f;
-            m = raise ? mx : m;
+            const float by = raise ? exp2_fast(m - low) : 1.0f;
+            m = raise ? low : m;
             l *= by;
 #pragma unroll
             for (int i = 0; i < DP / 32; i++) o[i] *= by;

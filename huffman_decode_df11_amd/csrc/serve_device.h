@@ -22,9 +22,14 @@ constexpr float kLn2 = 0.69314718055994530942f;
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // The two 16-bit element types: their matrix-core products, their rounding
-// from float32 (to nearest, ties to even) and the bits of a non-finite value.
+// from float32 (to nearest, ties to even), the bits of a non-finite value,
+// and the power of two that a row's greatest probability is held as (kLift):
+// float16 loses bits below 2^-14 and all of them below 2^-25, so its
+// probabilities stand 2^7 higher (with the 2^8 that the running maximum may
+// lag behind, 2^15 of at most 65504).
 struct Bf16 {
     static constexpr uint32_t kExpMask = 0x7f80u;
+    static constexpr float kLift = 0.0f;
     static __device__ __forceinline__ float value(uint32_t x) { return __builtin_bit_cast(float, x << 16); }
     static __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
     {
@@ -44,6 +49,7 @@ struct Bf16 {
 
 struct Fp16 {
     static constexpr uint32_t kExpMask = 0x7c00u;
+    static constexpr float kLift = 7.0f;
     static __device__ __forceinline__ float value(uint32_t x) { return (float)__builtin_bit_cast(_Float16, (uint16_t)x); }
     static __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
     {
@@ -70,7 +76,7 @@ __device__ __forceinline__ uint32_t order_of(float w)
     return w != w ? 0 : u ^ flip;
 }
 
-// The operands of a call, checked: E_ARG texts shared by the entry points.
+// A pointer for 16-byte loads and stores.
 inline bool aligned16(const void *p) { return p && !((uintptr_t)p & 15); }
 
 }  // namespace df11serve

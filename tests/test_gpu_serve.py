@@ -997,3 +997,36 @@ def test_cache_compact_within_one_allocation():
     for i, n in enumerate(("k", "v")):
         assert torch.equal(pool[i, :, :, :C].cpu(), x[n])
         assert torch.equal(pool[i, :, :, C:].cpu(), torch.where((want >= 0).unsqueeze(-1), x[n].gather(2, rows), 0))
+
+
+@pytest.mark.parametrize("path", ["few shared rows", "many shared rows", "own positions", "cache", "window"])
+def test_float16_keeps_small_probabilities(path):
+    """Every 32nd key has a logit of 17.046875, the others 0: 2^-24.6 of it each.
+    Only they have values (1000): half as much again would come out if their
+    probabilities were held as multiples of 2^-24 of the greatest.  The bound:
+    the result's rounding, 2^-12 for the sums, and a step of 2^-31 of the
+    greatest probability (half of it an error) for each of the 31 others, and
+    half of the result's own smallest step."""
+    n, big = 512, 17.046875
+    k, v = torch.zeros(n, 1, 64, dtype=HF), torch.full((n, 1, 64), 1000.0, dtype=HF)
+    k[::32, :, 0], v[::32] = big, 0.0
+    batch, tokens, heads = {"few shared rows": (1, 1, 4), "many shared rows": (24, 1, 4), "own positions": (3, 1, 4),
+                            "cache": (2, 1, 1), "window": (2, 40, 1)}[path]
+    q = torch.zeros(batch, tokens, heads, 64, dtype=HF, device="cuda")
+    q[..., 0] = 8.0
+    k, v = k.cuda(), v.cuda()
+    lengths = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    if "shared" in path:
+        out = serve.prefix_attention(q, k, v, k.expand(batch, n, 1, 64), v.expand(batch, n, 1, 64), 0 * lengths, scale=0.125)
+    elif path == "own positions":
+        out = serve.prefix_attention(q, k[:0], v[:0], k.expand(batch, n, 1, 64), v.expand(batch, n, 1, 64), lengths, scale=0.125)
+    else:
+        cache = serve.BoundedCache(k.view(1, 1, n, 64).repeat(batch, 1, 1, 1), v.view(1, 1, n, 64).repeat(batch, 1, 1, 1),
+                                   torch.zeros(batch, 1, n, device="cuda"),
+                                   torch.arange(n, dtype=torch.int32, device="cuda").repeat(batch, 1, 1), lengths)
+        out = serve.cache_attention(q, cache, lengths, scale=0.125)
+    small = np.exp(-big)
+    want = 31 * small * 1000 / (1 + 31 * small)
+    bound = (2.0 ** -11 + 2.0 ** -11 + 2.0 ** -12) * want + 2.0 ** -32 * 31 * 1000 + 2.0 ** -25
+    off = float((out.double() - want).abs().max())
+    assert off <= bound, (off, bound, want)
