@@ -1247,7 +1247,9 @@ int launch(const Args &a, hipStream_t st)
         a.prefix_places + places(a.suffix_tiles, (int64_t)a.batch * a.kv_heads * a.suffix_splits);
     const int64_t finish =
         (a.four ? ceil_div(a.rows, kWaves) : a.rows) + (KIND == kCache ? (int64_t)a.batch * a.kv_heads * ceil_div(a.suffix, kWeighKeys) : 0);
-    if (items > 0x7fffffffll || finish > 0x7fffffffll)
+    // a launch has fewer than 2^32 threads; refused here, none of a call's launches has begun
+    constexpr int64_t kMostGroups = 0xffffffffll / (64 * kWaves);
+    if (items > kMostGroups || finish > kMostGroups)
         return df11::fail(DF11_E_ARG, "attention: too many rows and keys for one launch");
     const dim3 block(64 * kWaves);
     if (items) hipLaunchKernelGGL((attend_kernel<E, DP, KIND>), dim3((uint32_t)items), block, 0, st, a);

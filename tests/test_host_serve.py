@@ -196,3 +196,15 @@ def test_caches_that_lie_on_each_other_are_not_cut_down(change):
     out = _cache(**{**apart, **change})
     assert L.df11_cache_compact(ctypes.byref(old), PTR, 4, 1, ctypes.byref(out), PTR, PTR + 64, None) == ARG
     assert b"in place" in L.df11_last_error()
+
+
+def test_attention_of_more_workgroups_than_a_launch_has_is_refused():
+    """Rows past what one launch joins (2^24 workgroups of four): refused before the first launch."""
+    L = _lib.lib()
+    a = _prefix(batch=1 << 10, tokens=1 << 12, heads=1 << 8, kv_heads=2, dim=8)
+    assert L.df11_prefix_attention_workspace_bytes(ctypes.byref(a)) > 0
+    assert L.df11_prefix_attention(ctypes.byref(a), PTR, (1 << 63) - 1, None) == ARG
+    c = _cache(batch=1 << 10)
+    t = _attend(tokens=1 << 12, heads=1 << 8)
+    assert L.df11_cache_attention(ctypes.byref(c), ctypes.byref(t), PTR, (1 << 63) - 1, None) == ARG
+    assert b"one launch" in L.df11_last_error()
