@@ -63,7 +63,7 @@ struct Args {
     float2 *part_ml;           // [slot][row]
     float *tops;               // many rows of a cache: a row's logarithm (base 2) of its sum, +infinity if it is empty
     float *logits;             // few rows: [batch * kv_heads][rows of a head][logit_stride]
-    int32_t batch, tokens, heads, kv_heads, group, dim, prefix, suffix, page, n_pages, fp16;
+    int32_t batch, tokens, heads, kv_heads, group, dim, prefix, suffix, page, n_pages;
     int64_t q_batch, q_token, q_head, prefix_token, prefix_head, k_batch, k_token, k_head, table_batch;
     int64_t logit_stride;
     float scale2;              // scale * log2(e)
@@ -387,9 +387,9 @@ __device__ __forceinline__ void attend_wave(const Src &src, const u32x4 (&q)[DP 
 // different banks (k_at, v_at).
 // 32 rows a wave: a wave's operands from LDS are as many cycles as its
 // products, and 64 rows would leave one wave a SIMD (its sums alone 128
-// registers).  128 requests behind 32768 positions, 70 GFLOP: 84 us, 830
-// TFLOP/s; matrix cores, vector ALU and LDS are each busy about a third of
-// the time, one phase of a step behind the other.
+// registers).  128 requests behind 32768 positions, 70 GFLOP: 90 us, 785
+// TFLOP/s; matrix cores are busy 40% of the time, the vector ALU 45% and LDS
+// 37%, one phase of a step mostly behind the other.
 constexpr int kTileRows = 32 * kWaves;
 
 // Rows up to this many elements apart go into 128-row tiles: a lane's distance
@@ -1183,9 +1183,10 @@ void plan(Args &a, bool cache)
     a.suffix_tiles = ceil_div(own_rows, cache && a.big ? kTileRows : kRows);
     // 128-row tiles: one workgroup on each CU, whose partial sums are few and
     // which leaves room for those of the sequences' own positions; two where
-    // a long prefix is nearly all there is (128 requests behind 32768
-    // positions with 1024 / 1 of their own: 137 / 130 us with one, 157 / 109
-    // with two; 64 requests behind 8191: 29 us with one, 37 with two).
+    // a long prefix is nearly all there is (attention and join of 128 requests
+    // behind 32768 positions with 1024 / 1 of their own: 136 / 106 us with one,
+    // 157 / 100 with two; of 64 behind 8191 with 700 / 1: 45 / 29 us with one,
+    // 51 / 37 with two).
     const int64_t prefix_items = (int64_t)a.prefix_tiles * a.kv_heads;
     const bool alone = 4ll * a.batch * a.suffix <= a.prefix && a.prefix * prefix_items >= 2048 * cus;
     set_ranges(a.prefix, a.big ? (alone ? 2 : 1) * cus / prefix_items : ranges_that_fill(a.prefix, prefix_items, resident * cus),
