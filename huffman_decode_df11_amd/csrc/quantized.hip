@@ -1443,8 +1443,9 @@ __global__ void __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) tile_kernel(const 
     };
     const int v_to = S::v_at(v_word * 8, v_key / 16 * 2 + (v_key / 4 & 1)) + (v_key / 8 & 1) * 8 + v_key % 4 * 2;
     // A value that a row does not see has weight 0 there, so it must be a
-    // number: of keys that no row sees it is 0; of those that some see it is
-    // too, if it is none, and comes last (below).
+    // number: of keys that no row of the tile sees it is 0 (as a finite one it
+    // might pass float16: find_scale looks at the keys below key1); of those that some
+    // see it is too, if it is none, and comes last (below).
     const auto clear = [&](int to, int base) {
         const bool whole = __all(v_there);
         if (!whole || base + kKeys > all) {
@@ -1455,7 +1456,7 @@ __global__ void __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) tile_kernel(const 
                 for (int i = 0; i < G; i++) {
                     const uint32_t x = vp[j][i];
                     const bool number = (x & E::kExpMask) != E::kExpMask && (x >> 16 & E::kExpMask) != E::kExpMask;
-                    const bool seen = v_there && key + j < n;
+                    const bool seen = v_there && key + j < key1;
                     if (seen && key + j >= all && !number) odd = 1;
                     if (!seen || (key + j >= all && !number)) vp[j][i] = 0;
                 }

@@ -1,0 +1,71 @@
+"""The quantised cache's operators where values, tiles and layouts meet their
+ends: values that a row must not see beside ones that it does, groups near the ends of
+a type's range, and outputs that lie on inputs."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import quantized_reference as ref  # noqa: E402
+from huffman_decode_df11_amd import _lib, serve  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+BF, HF, I32 = torch.bfloat16, torch.float16, torch.int32
+INF, NAN = float("inf"), float("nan")
+MANY = 112   # rows that share a key head's keys up to which values are not made
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _randn(g, *shape, dtype=BF, scale=1.0):
+    return (scale * torch.randn(shape, generator=g)).to(dtype)
+
+
+def _held(k, v):
+    """Codes and pairs of rows k, v [pages, H, page, D], on the CPU."""
+    (kc, ks, km), (vc, vs, vm) = ref.quantise(k), ref.quantise(v)
+    return [ref.packed(kc), ref.packed(vc), torch.stack([ks, km], -1), torch.stack([vs, vm], -1)]
+
+
+def _on_gpu(parts):
+    return serve.QuantizedCache(*(t.cuda() for t in parts))
+
+
+def _check(q, parts, lengths, table, what, scale=None):
+    """Output and lse of every row within their bounds."""
+    print("case", what, flush=True)
+    n = torch.tensor(lengths, dtype=I32)
+    many = q.shape[1] * q.shape[2] // parts[0].shape[1] > MANY
+    out, lse = serve.quantized_attention(q.cuda(), _on_gpu(parts), n.cuda(), block_table=table.cuda(), scale=scale, return_lse=True)
+    torch.cuda.synchronize()
+    want, want_lse, bound = ref.attention(q, parts, n, table, scale, many)
+    got, got_lse = out.cpu().double(), lse.cpu().double()
+    assert torch.equal(torch.isfinite(got), torch.isfinite(want)), what
+    # a result below the type's normal range (2^-14 in float16) is rounded to a whole smallest number, off by up to half of one
+    off = (got - want).abs() - bound - torch.finfo(q.dtype).smallest_normal * torch.finfo(q.dtype).eps / 2
+    assert float(off.nan_to_num(nan=-1.0).max()) <= 1e-30, (what, float(off.nan_to_num(nan=-1.0).max()))
+    return got, got_lse, want_lse
+
+
+@pytest.mark.parametrize("times", [8.0, 2.0 ** 15, "alone"])
+@pytest.mark.parametrize("dtype,D", [(BF, 64), (HF, 64), (BF, 128), (HF, 128), (BF, 256), (HF, 256)])
+def test_values_behind_a_tiles_last_key(dtype, D, times):
+    """640 rows of 160 tokens are several tiles, whose last keys lie inside a
+    step; V of the positions right behind each tile's last one is up to 2^15
+    times the others', or the others are zero.  No row of the tile sees them."""
+    g = _gen(D)
+    T, n, page = 160, 197, 16
+    v = _randn(g, 15, 1, page, D, dtype=dtype, scale=2.0 ** -6)
+    parts = _held(_randn(g, 15, 1, page, D, dtype=dtype), v)
+    table = torch.randperm(15, generator=g)[:13].view(1, 13).to(I32)
+    if times == "alone":
+        kept, parts[3] = parts[3], torch.zeros_like(parts[3])
+    for tile in range(32 if D == 256 else 64, T, 32 if D == 256 else 64):
+        for s in (n - T + tile, n - T + tile + 5):   # the first key that the rows before token `tile` do not see
+            at = (table[0, s // page].long(), slice(None), s % page)
+            parts[3][at] = kept[at] if times == "alone" else parts[3][at] * times
+    _check(_randn(g, 1, T, 4, D, dtype=dtype), parts, [n], table, (dtype, D, times))
