@@ -107,9 +107,12 @@ __device__ __forceinline__ i16x2 over_lanes(i16x2 x, F &&join)
 // A code is floor((x - least) / step + 1/2): the quotient by the inverse, with
 // 2^-18 more than 1/2 (x - least and the inverse err by 2^-23 of at most 16),
 // has the code or one more as its floor, and (code - 1/2) * step, 13 bits, says
-// which.  Where x - least is not exact (seldom: their exponents differ by more
-// than 13), or the step so small that its inverse may not be a number, 64 bits
-// are taken.
+// which.  64 bits are taken where x - least is not exact, which is seldom, or the step so small
+// that its inverse may not be a number.  The difference d is exact if d +
+// least is x again and least is no larger than x, or is larger but not
+// below 2^-8 of the step: x is at most 2^12 times it then, and all are multiples
+// of 2^-11 of it or more, which 24 bits hold.  (A smaller one, but 0, vanishes in d and
+// in d + least alike, and a value on a border has the code below: all of such a row in 64 bits.)
 template <class E, int DP>
 __device__ __forceinline__ void quantise(const u32x4 (&raw)[2], u32x2 &codes, uint32_t (&pairs)[RowLanes<DP>::G])
 {
@@ -146,7 +149,7 @@ __device__ __forceinline__ void quantise(const u32x4 (&raw)[2], u32x2 &codes, ui
         low[g] = E::value(pairs[g] >> 16);
         half[g] = -0.5f * step[g];
         inverse[g] = step[g] > 0.0f ? __builtin_amdgcn_rcpf(step[g]) : 0.0f;   // errs by 2^-23
-        exact = exact && !(step[g] < 0x1p-100f);
+        exact = exact && !(step[g] < 0x1p-100f) && !(__builtin_fabsf(low[g]) < 0x1p-8f * step[g] && low[g] != 0.0f);
     });
     float c[16];
     bool differs[16];

@@ -69,3 +69,39 @@ def test_values_behind_a_tiles_last_key(dtype, D, times):
             at = (table[0, s // page].long(), slice(None), s % page)
             parts[3][at] = kept[at] if times == "alone" else parts[3][at] * times
     _check(_randn(g, 1, T, 4, D, dtype=dtype), parts, [n], table, (dtype, D, times))
+
+
+def _write(k):
+    """Codes and pairs of rows k [n, 64] as they are written, and the same rows' in 64 bits."""
+    n = k.shape[0]
+    per = -(-n // 16)
+    cache = serve.QuantizedCache.empty(per, 1, 16, 64, dtype=k.dtype)
+    rows, table = k[None, :, None].cuda(), torch.arange(per, dtype=I32, device="cuda").view(1, per)
+    serve.quantized_write(cache, rows, rows, torch.zeros(1, dtype=I32, device="cuda"), block_table=table)
+    codes, step, least = ref.quantise(k)
+    for c, s in ((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales)):
+        assert torch.equal(s.cpu().flatten(0, 2)[:n], torch.stack([step, least], -1))
+        yield ref.unpacked(c.cpu().flatten(0, 2)[:n]), codes
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_codes_of_values_on_a_border_over_a_tiny_least_value(dtype):
+    """A border of the steps from 0 is missed by as much as the least value
+    lies above 0 (or passed, below 0), however little that is."""
+    g, rows = _gen(1), []
+    groups = [(2.0 ** -24, 2.0, 60.0), (2.0 ** -24, 7.5, 15.0), (2.0 ** -20, 0.5, 15.0)]
+    if dtype == BF:
+        groups += [(2.0 ** -30, 1.0, 30.0), (2.0 ** -26, 3.0, 30.0), (2.0 ** -30, 0.5, 15.0), (2.0 ** -50, 10.5, 15.0)]
+    for least, on, greatest in groups:
+        row = torch.full((64,), on, dtype=torch.float64)
+        row[::8], row[3::8], row[4::8], row[7::8] = least, least, greatest, greatest
+        rows.append(row)
+    for _ in range(3000):   # values on borders of steps that are powers of two, over least values down to 2^-40 of one
+        step = 2.0 ** int(torch.randint(-6, 7, (1,), generator=g))
+        row = (torch.randint(0, 15, (64,), generator=g).double() + 0.5) * step
+        least = step * 2.0 ** -float(torch.randint(0, 41, (1,), generator=g)) * (1 if len(rows) % 2 else -1)
+        row[:2], row[2:4] = least, 15 * step
+        rows.append(row)
+    for got, want in _write(torch.stack(rows).to(dtype)):
+        wrong = (got != want).any(-1).nonzero().flatten()
+        assert not wrong.numel(), (wrong.numel(), wrong[:5].tolist(), [rows[i][:4].tolist() for i in wrong[:2]])
