@@ -1098,10 +1098,14 @@ __device__ __forceinline__ void join_waves(const Args &a, Wave<E, DP, NT> &x, in
     }
 }
 
-// A power of two that leaves x / it below 16, and its inverse.
+// A power of two that leaves x / it below 16, and its inverse: float16 has bits
+// down to 2^-24 for three parts of that.  bfloat16 has them for any number, and steps
+// near float32's end, which are multiplied by kOff times that: below 2^-8 there.
+template <class E>
 __device__ __forceinline__ float power_below(float x, float &inverse)
 {
-    const uint32_t e = __builtin_bit_cast(uint32_t, x) >> 23, power = e < 8 ? 127 : e - 3;
+    const uint32_t e = __builtin_bit_cast(uint32_t, x) >> 23;
+    const uint32_t power = std::is_same_v<E, Bf16> ? min(e + 9, 253u) : e < 8 ? 127 : e - 3;
     inverse = __builtin_bit_cast(float, (254 - power) << 23);
     return __builtin_bit_cast(float, power << 23);
 }
@@ -1178,7 +1182,7 @@ __global__ void __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) attend_kernel(
             sum[i] += __shfl_xor(sum[i], 32);
             most = fmaxf(most, fabsf(sum[i]));
         }
-        qf[t] = power_below(most, inverse);
+        qf[t] = power_below<E>(most, inverse);
 #pragma unroll
         for (int i = 0; i < 4; i++) qb[t][i] = i < G && g < 3 ? part_pair<E>(sum[i % G] * inverse, g) : 0;
     }
@@ -1240,7 +1244,7 @@ __global__ void __launch_bounds__(64 * kWaves, DP == 256 ? 2 : DP == 128 ? 3 : 4
                 sum[i] = over_blocks(sum[i], [](float u, float v) { return u + v; });
                 most = fmaxf(most, fabsf(sum[i]));
             }
-            const float power = power_below(most, inverse);
+            const float power = power_below<E>(most, inverse);
             if (lane < kFew) {
 #pragma unroll
                 for (int k = 0; k < 3; k++)
@@ -1302,12 +1306,17 @@ __global__ void __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) tile_kernel(const 
     constexpr int kPair = kKeys * kWords / kThreads;        // keys of a thread's word of V
     static_assert(kEach == 4 || kEach == 2, "");
     constexpr int kNumbers = std::is_same_v<E, Fp16> ? 2 : 1;   // float16 to a value of V
+    // K is made times a power of two: the greatest code may stand for more than
+    // the type's greatest number, since the step is rounded, and bfloat16's 16 steps for
+    // more than float32's.
+    constexpr float kKeyPower = std::is_same_v<E, Fp16> ? 0.5f : 0.25f;
     constexpr int kHalf = kKeys * DP * 2, kBuffer = (2 + kNumbers) * kHalf;   // a step's K, V^T, and what is left of K (and V)
     __shared__ alignas(1024) char lds[2 * kBuffer];
     __shared__ uint64_t pages[2];   // a byte for each 16 keys of a step: whether there is a page
     __shared__ int odd;             // whether some of V is no number for some rows
     __shared__ uint32_t top, bottom;   // bits of the greatest and the least bound of a group of V
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31, g = lane >> 5;
+    const float scale2 = a.scale2 / kKeyPower;
     Item it = item_of(a);
     if (!it.some) return;
     const int row_count = a.tokens * a.group, n = it.n, all = n - a.tokens + 1;
@@ -1472,7 +1481,7 @@ __global__ void __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) tile_kernel(const 
 #pragma unroll
         for (int w = 0; w < kEach; w++) {
             float y[8];
-            values(kx[w], kp, std::true_type{}, 1.0f, y);
+            values(kx[w], kp, std::true_type{}, kKeyPower, y);
             u32x4 x, left;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
@@ -1562,7 +1571,7 @@ __global__ void __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) tile_kernel(const 
         for (int k = 0; k < kParts; k++)
 #pragma unroll
             for (int r = 0; r < 16; r++) mx = fmaxf(mx, s[k][r]);
-        mx = fmaxf(mx, __shfl_xor(mx, 32)) * a.scale2;
+        mx = fmaxf(mx, __shfl_xor(mx, 32)) * scale2;
         const float low = mx - N::kLift;   // as in attend_wave
         const bool raise = low > m + 8.0f;
         if (__any(raise)) {
@@ -1580,8 +1589,8 @@ __global__ void __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) tile_kernel(const 
                 u32x4 pb;
 #pragma unroll
                 for (int w = 0; w < 4; w++) {
-                    const float x = exp2_fast(__builtin_fmaf(s[k][8 * half + 2 * w], a.scale2, -safe));
-                    const float y = exp2_fast(__builtin_fmaf(s[k][8 * half + 2 * w + 1], a.scale2, -safe));
+                    const float x = exp2_fast(__builtin_fmaf(s[k][8 * half + 2 * w], scale2, -safe));
+                    const float y = exp2_fast(__builtin_fmaf(s[k][8 * half + 2 * w + 1], scale2, -safe));
                     l += x + y;
                     pb[w] = N::pack(x, y);
                 }
@@ -1857,7 +1866,8 @@ int make_attention(const df11_quantized_cache *c, const df11_quantized_attention
     a.batch = p->batch, a.tokens = p->tokens, a.heads = p->heads, a.group = p->heads / c->kv_heads;
     a.q_batch = p->q_batch, a.q_token = p->q_token, a.q_head = p->q_head;
     a.scale2 = (float)(p->scale * 1.44269504088896340736);
-    if (!(a.scale2 > 0.0f && a.scale2 < INFINITY)) return df11::fail(DF11_E_ARG, "%s: scale must be positive", who);
+    if (!(a.scale2 > 0.0f && a.scale2 < 0x1p126f))   // tile_kernel takes four times that
+        return df11::fail(DF11_E_ARG, "%s: scale must be positive and below 2^125", who);
     plan(a);
     return DF11_OK;
 }

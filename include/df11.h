@@ -664,6 +664,8 @@ int df11_quantized_read(const df11_quantized_cache *c, const df11_quantized_read
  * Up to 112 rows, or where V is so far apart, values of V past 2^104 may come
  * out infinite or NaN, and float16 holds a probability times a step to 2^-31 of
  * the greatest step among a sequence's positions, seen or not.
+ * K may be what any finite row is written as; scale is positive and below
+ * 2^125; logits past float32's range are no numbers.
  * Workspace and errors as df11_prefix_attention; the result does not depend
  * on the run. */
 typedef struct df11_quantized_attention_args {

@@ -105,3 +105,25 @@ def test_codes_of_values_on_a_border_over_a_tiny_least_value(dtype):
     for got, want in _write(torch.stack(rows).to(dtype)):
         wrong = (got != want).any(-1).nonzero().flatten()
         assert not wrong.numel(), (wrong.numel(), wrong[:5].tolist(), [rows[i][:4].tolist() for i in wrong[:2]])
+
+
+@pytest.mark.parametrize("T", [1, 10, 65])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_keys_at_the_ends_of_the_range(dtype, T):
+    """Groups that reach the type's greatest number: the step is rounded, so
+    that the greatest code may stand for more than that."""
+    g = _gen(T)
+    top = float(torch.finfo(dtype).max)
+    least = -top if dtype == HF else -2.0 ** 120
+    k = _randn(g, 6, 1, 16, 128, dtype=dtype)
+    k[:, :, ::3, 5], k[:, :, ::3, 9], k[:, :, 1::3, 4], k[:, :, 1::3, 7] = top, least, -top, top
+    parts = _held(k, _randn(g, 6, 1, 16, 128, dtype=dtype))
+    past = (15 * parts[2][..., 0].double() + parts[2][..., 1].double()).max()
+    assert past > top
+    # logits of a size near 1 at the least and greatest numbers
+    small = 2.0 ** -12 if dtype == HF else 2.0 ** -112
+    q, scale = _randn(g, 1, T, 2, 128, dtype=dtype, scale=small), 2.0 ** -4 if dtype == HF else 2.0 ** -16
+    _, lse, want_lse = _check(q, parts, [70], torch.tensor([[3, 1, 0, 5, 2]], dtype=I32), (dtype, T), scale)
+    # logits: sums of |q| (143 or 31) step in float32, K to 2^-16 (bfloat16) or 2^-20 of its values
+    reach = scale * float(q.double().abs().sum(-1).max()) * float(parts[2][..., 0].double().abs().max())
+    assert float((lse - want_lse).abs().max()) <= 2.0 ** -12 + (2.0 ** -20 * 143 + 2.0 ** -16 * 15) * reach
