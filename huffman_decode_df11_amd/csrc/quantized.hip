@@ -336,8 +336,8 @@ struct Args {
     const int32_t *lengths;
     uint16_t *out;
     float *lse;
-    float *part_o;     // [split][row][dim]
-    float2 *part_ml;   // [split][row]
+    float *part_o;     // [split][row][dim]: a range's own result, which no number of keys makes greater than its values
+    float2 *part_ml;   // [split][row]: the power of two that its sum of probabilities is held below, and that sum
     int32_t batch, tokens, heads, group, tiles, splits, granule;
     int64_t q_batch, q_token, q_head, rows;
     float scale2;      // scale * log2(e)
@@ -1086,12 +1086,12 @@ __device__ __forceinline__ void join_waves(const Args &a, Wave<E, DP, NT> &x, in
                 u += f * join_o[w][r][d], v += f * join_o[w][r][d + 1];
             }
             const int64_t row = ((int64_t)b * a.tokens + at / a.group) * a.heads + head * a.group + at % a.group;
+            const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
             if (a.splits == 1) {
-                const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
                 *(uint32_t *)(a.out + row * a.c.dim + d) = E::pack(u * inv, v * inv);
                 if (d == 0) put_lse(a, row, mm, ll);
             } else {
-                *(float2 *)(a.part_o + (split * a.rows + row) * a.c.dim + d) = make_float2(u, v);
+                *(float2 *)(a.part_o + (split * a.rows + row) * a.c.dim + d) = make_float2(u * inv, v * inv);
                 if (d == 0) a.part_ml[split * a.rows + row] = make_float2(mm, ll);
             }
         }
@@ -1314,7 +1314,7 @@ __global__ void __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) tile_kernel(const 
     __shared__ alignas(1024) char lds[2 * kBuffer];
     __shared__ uint64_t pages[2];   // a byte for each 16 keys of a step: whether there is a page
     __shared__ int odd;             // whether some of V is no number for some rows
-    __shared__ uint32_t top, bottom;   // bits of the greatest and the least bound of a group of V
+    __shared__ uint32_t top, bottom;   // bits of a 32nd of the greatest and the least bound of a group of V
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31, g = lane >> 5;
     const float scale2 = a.scale2 / kKeyPower;
     Item it = item_of(a);
@@ -1418,7 +1418,8 @@ __global__ void __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) tile_kernel(const 
             for (int j = 0; j < 4; j++)
 #pragma unroll
                 for (int i = 0; i < G; i++) {
-                    const float x = fabsf(E::value(pairs[j][i] >> 16)) + 15.0f * fabsf(E::value(pairs[j][i] & 0xffffu));
+                    // a 32nd of the bound, which no number of the type brings past float32's range
+                    const float x = __builtin_fmaf(15.0f / 32, fabsf(E::value(pairs[j][i] & 0xffffu)), fabsf(E::value(pairs[j][i] >> 16)) / 32);
                     most = there[j] && x < INFINITY ? fmaxf(most, x) : most;
                     least = there[j] && x > 0.0f ? fminf(least, x) : least;
                 }
@@ -1428,7 +1429,7 @@ __global__ void __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) tile_kernel(const 
         if (lane == 0) atomicMax(&top, __builtin_bit_cast(uint32_t, most)), atomicMin(&bottom, __builtin_bit_cast(uint32_t, least));
         lds_barrier();
         if (__builtin_bit_cast(float, top) > 0x1p20f * __builtin_bit_cast(float, bottom)) return false;
-        const int power = (int)(top >> 23) - 127;   // a range without values: -127
+        const int power = (int)(top >> 23) - 127 + 5;   // a range without values: -122
         v_scale = __builtin_ldexpf(1.0f, min(14 - power, 126));
         return true;
     };
@@ -1666,8 +1667,8 @@ __global__ void __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) tile_kernel(const 
     l += __shfl_xor(l, 32);
     if (row >= row_count) return;
     const int64_t out_row = ((int64_t)it.b * a.tokens + token) * a.heads + h;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     if (a.splits == 1) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
         for (int i = 0; i < DP / 32; i++)
 #pragma unroll
@@ -1685,7 +1686,7 @@ __global__ void __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) tile_kernel(const 
 #pragma unroll
             for (int r = 0; r < 16; r += 4) {
                 const int d = 32 * i + 2 * r + 4 * g;
-                if (d < dim) *(f32x4 *)(to + d) = f32x4{o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]} * unscale;
+                if (d < dim) *(f32x4 *)(to + d) = f32x4{o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]} * inv * unscale;
             }
         if (g == 0) a.part_ml[it.split * a.rows + out_row] = make_float2(m, l);
     }
@@ -1712,13 +1713,16 @@ __global__ void __launch_bounds__(64 * kWaves) join_kernel(const Args a)
 #pragma unroll
     for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
     const float safe = m == -INFINITY ? 0.0f : m;
-    const float factor = exp2_fast(mine.x - safe);
-    float l = factor * mine.y;
+    const float part = exp2_fast(mine.x - safe) * mine.y;
+    float l = part;
 #pragma unroll
     for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float factor = part * (l == 0.0f ? 0.0f : 1.0f / l);
     constexpr int kBy = WIDE ? kWaves : 1;
-    for (int d = 2 * lane; d < a.c.dim; d += 128) {
+    // every lane goes through the sums, those behind the last dim with that one once
+    // more: each holds the factor of a range, which the others read
+    for (int d0 = 0; d0 < a.c.dim; d0 += 128) {
+        const int d = min(d0 + 2 * lane, a.c.dim - 2);
         float x = 0.0f, y = 0.0f;
         for (int s0 = WIDE ? wave : 0; s0 < a.splits; s0 += 8 * kBy) {
             float2 o[8];
@@ -1736,7 +1740,7 @@ __global__ void __launch_bounds__(64 * kWaves) join_kernel(const Args a)
             }
         }
         if (WIDE) sums[wave][d / 2] = make_float2(x, y);
-        else *(uint32_t *)(a.out + row * a.c.dim + d) = E::pack(x * inv, y * inv);
+        else *(uint32_t *)(a.out + row * a.c.dim + d) = E::pack(x, y);
     }
     if (WIDE) {
         __syncthreads();
@@ -1744,7 +1748,7 @@ __global__ void __launch_bounds__(64 * kWaves) join_kernel(const Args a)
             float x = 0.0f, y = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWaves; w++) x += sums[w][threadIdx.x].x, y += sums[w][threadIdx.x].y;
-            *(uint32_t *)(a.out + row * a.c.dim + 2 * threadIdx.x) = E::pack(x * inv, y * inv);
+            *(uint32_t *)(a.out + row * a.c.dim + 2 * threadIdx.x) = E::pack(x, y);
         }
     }
     if (lane == 0 && (!WIDE || wave == 0)) put_lse(a, row, m, l);

@@ -277,7 +277,7 @@ def quantized_attention(q, cache: QuantizedCache, lengths, *, block_table=None, 
     positions (int32); token t sees the first lengths - T + 1 + t of them.
     Returns out [B, T, Hq, D], and with return_lse also lse [B, T, Hq]
     float32.  A row that sees no position is zero (lse -inf).  Values of V stay
-    below 2^104 in size: past that up to 112 rows may come out infinite or NaN."""
+    below 2^115 / lengths in size: past that up to 112 rows may come out infinite or NaN."""
     if _elsewhere(cache.k_codes, stream):
         with _there(cache.k_codes, stream):
             return quantized_attention(q, cache, lengths, block_table=block_table, scale=scale, out=out, return_lse=return_lse)

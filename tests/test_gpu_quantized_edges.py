@@ -127,3 +127,15 @@ def test_keys_at_the_ends_of_the_range(dtype, T):
     # logits: sums of |q| (143 or 31) step in float32, K to 2^-16 (bfloat16) or 2^-20 of its values
     reach = scale * float(q.double().abs().sum(-1).max()) * float(parts[2][..., 0].double().abs().max())
     assert float((lse - want_lse).abs().max()) <= 2.0 ** -12 + (2.0 ** -20 * 143 + 2.0 ** -16 * 15) * reach
+
+
+@pytest.mark.parametrize("n", [70, 3000])
+@pytest.mark.parametrize("scale", [2.0 ** 120, 2.0 ** 126.9])
+def test_many_rows_over_values_at_the_end_of_the_range(scale, n):
+    """V of bfloat16 up to its greatest number, in one range of keys and in several."""
+    g = _gen(n)
+    per = -(-n // 16)
+    v = (torch.randn((per, 1, 16, 64), generator=g).clamp(-1.0, 1.0).double() * scale).to(BF)
+    parts = _held(_randn(g, per, 1, 16, 64), v)
+    assert torch.isfinite(v).all() and torch.isfinite(parts[3]).all()
+    _check(_randn(g, 1, 65, 2, 64), parts, [n], torch.randperm(per, generator=g).view(1, per).to(I32), (scale, n))
