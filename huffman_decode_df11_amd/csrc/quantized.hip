@@ -1428,10 +1428,11 @@ __global__ void __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) tile_kernel(const 
         for (int d = 32; d; d >>= 1) most = fmaxf(most, __shfl_xor(most, d)), least = fminf(least, __shfl_xor(least, d));
         if (lane == 0) atomicMax(&top, __builtin_bit_cast(uint32_t, most)), atomicMin(&bottom, __builtin_bit_cast(uint32_t, least));
         lds_barrier();
-        if (__builtin_bit_cast(float, top) > 0x1p20f * __builtin_bit_cast(float, bottom)) return false;
+        const bool apart = __builtin_bit_cast(float, top) > 0x1p20f * __builtin_bit_cast(float, bottom);
         const int power = (int)(top >> 23) - 127 + 5;   // a range without values: -122
-        v_scale = __builtin_ldexpf(1.0f, min(14 - power, 126));
-        return true;
+        // Far apart: as they are, for the small ones' sake, but for what float16 would not hold
+        if (!apart || std::is_same_v<E, Fp16>) v_scale = __builtin_ldexpf(1.0f, min(14 - power, apart ? 0 : 126));
+        return !apart;
     };
     // The values of a word's eight codes.
     const auto values = [&](uint32_t w, const uint32_t (&pairs)[G], auto exact, float by, float (&y)[8]) {

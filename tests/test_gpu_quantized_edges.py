@@ -139,3 +139,16 @@ def test_many_rows_over_values_at_the_end_of_the_range(scale, n):
     parts = _held(_randn(g, per, 1, 16, 64), v)
     assert torch.isfinite(v).all() and torch.isfinite(parts[3]).all()
     _check(_randn(g, 1, 65, 2, 64), parts, [n], torch.randperm(per, generator=g).view(1, per).to(I32), (scale, n))
+
+
+def test_many_rows_over_float16_values_from_end_to_end():
+    """One position's V spans float16's range and its greatest code stands for
+    65536; the others' are 2^20 smaller and less."""
+    g = _gen(7)
+    v = _randn(g, 6, 1, 16, 128, dtype=HF, scale=2.0 ** -9)
+    v[4, 0, 3, ::2], v[4, 0, 3, 1::2] = 65504.0, -65504.0
+    v[4, 0, 3, 4:8] = torch.tensor([-65504.0, 65504.0, -65504.0, 65504.0])
+    parts = _held(_randn(g, 6, 1, 16, 128, dtype=HF), v)
+    assert float((15 * parts[3][..., 0].double() + parts[3][..., 1].double()).max()) == 65536.0
+    got, _, _ = _check(_randn(g, 1, 65, 2, 128, dtype=HF), parts, [90], torch.tensor([[3, 4, 0, 5, 2, 1]], dtype=I32), "end to end")
+    assert torch.isfinite(got).all()
