@@ -283,12 +283,23 @@ __global__ void __launch_bounds__(kMoveThreads) read_kernel(const ReadArgs a)
             u32x4 y = {};
             if (there[r]) {
                 const uint32_t low = w[which][r] & 0x0f0f0f0fu, high = w[which][r] >> 4 & 0x0f0f0f0fu;
+                float step[G], least[G], x[8];
+                bool past = false;   // a code may stand for more than the type's greatest number, since the step is rounded
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const uint32_t p = pairs[which][r][2 * i % G], q = pairs[which][r][(2 * i + 1) % G];
-                    y[i] = E::pack(__builtin_fmaf((float)(low >> (8 * i) & 255u), E::value(p & 0xffffu), E::value(p >> 16)),
-                                   __builtin_fmaf((float)(high >> (8 * i) & 255u), E::value(q & 0xffffu), E::value(q >> 16)));
+                for (int i = 0; i < G; i++) {
+                    step[i] = E::value(pairs[which][r][i] & 0xffffu), least[i] = E::value(pairs[which][r][i] >> 16);
+                    past = past || __builtin_fabsf(__builtin_fmaf(15.0f, step[i], least[i])) > E::kMost;
                 }
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    x[i] = __builtin_fmaf((float)((i % 2 ? high : low) >> (8 * (i / 2)) & 255u), step[i % G], least[i % G]);
+                if (past)
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        if (__builtin_fabsf(step[i % G]) <= E::kMost && __builtin_fabsf(least[i % G]) <= E::kMost)
+                            x[i] = __builtin_amdgcn_fmed3f(x[i], -E::kMost, E::kMost);
+#pragma unroll
+                for (int i = 0; i < 4; i++) y[i] = E::pack(x[2 * i], x[2 * i + 1]);
             }
             __builtin_nontemporal_store(y, (u32x4 *)((which ? a.v : a.k) + out + (int64_t)r * a.c.kv_heads * a.c.dim));
         }

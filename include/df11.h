@@ -638,7 +638,9 @@ int df11_quantized_write(const df11_quantized_cache *c, const df11_quantized_wri
 
 /* k, v [batch, count, kv_heads, dim], contiguous: the positions first[b] ..
  * first[b] + count - 1 (from 0 where first is NULL) of sequence b as the
- * values they stand for, rounded once to the cache's type; zeros from
+ * values they stand for, taken in float32 and rounded to the cache's type, those
+ * of numbers past its greatest one to that (the step of a group is rounded, so
+ * that code 15 may stand for more than what was written); zeros from
  * lengths[b] on and where nothing is held.  Errors as df11_quantized_write. */
 typedef struct df11_quantized_read_args {
     void *k, *v;

@@ -152,3 +152,28 @@ def test_many_rows_over_float16_values_from_end_to_end():
     assert float((15 * parts[3][..., 0].double() + parts[3][..., 1].double()).max()) == 65536.0
     got, _, _ = _check(_randn(g, 1, 65, 2, 128, dtype=HF), parts, [90], torch.tensor([[3, 4, 0, 5, 2, 1]], dtype=I32), "end to end")
     assert torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_finite_rows_are_read_back_finite(dtype):
+    """A code may stand for more than the type's greatest number (the step is
+    rounded): it is read as that; what has no number stays without one."""
+    top = float(torch.finfo(dtype).max)
+    rows = torch.zeros((5, 64), dtype=dtype)
+    rows[0, ::2], rows[0, 1::2] = (torch.linspace(0, 1, 32) * top).to(dtype), (torch.linspace(-1, 1, 32) * top).to(dtype)
+    rows[1, 2:4], rows[1, 8:10] = top, -top if dtype == HF else -2.0 ** 120
+    rows[2, 7], rows[3, 6], rows[4, 5] = NAN, INF, -INF
+    cache = serve.QuantizedCache.empty(1, 1, 16, 64, dtype=dtype)
+    one = lambda x: torch.full((1,), x, dtype=I32, device="cuda")   # noqa: E731
+    serve.quantized_write(cache, rows[None, :, None].cuda(), rows[None, :, None].flip(1).cuda(), one(0))
+    cache.k_scales[0, 0, 6, 0, 1] = INF   # as no write makes them
+    cache.k_scales[0, 0, 7, 1, 0] = -INF
+    k, v = (x.cpu()[0, :, 0] for x in serve.quantized_read(cache, one(9), 9))
+    codes, step, least = ref.quantise(rows)
+    want = codes.double() * ref.spread(step.double(), 64) + ref.spread(least.double(), 64)
+    assert want[:2].max() > top
+    want = want.clamp(-top, top).float().to(dtype)
+    for got, w in ((k[:5], want), (v[:5], want.flip(0))):
+        assert torch.equal(torch.isnan(got), torch.isnan(w)) and torch.equal(got.nan_to_num(), w.nan_to_num())
+    assert torch.isfinite(k[:2]).all() and float(k[:2].max()) == top
+    assert not torch.isfinite(k[6, ::2]).any() and not k[6, 1::2].any() and not torch.isfinite(k[7, 1::2]).any()
