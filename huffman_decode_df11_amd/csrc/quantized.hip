@@ -16,6 +16,7 @@
 #include <utility>
 
 #include "df11_internal.h"
+#include "overlap.h"
 #include "serve_device.h"
 
 namespace {
@@ -1768,6 +1769,21 @@ __global__ void __launch_bounds__(64 * kWaves) join_kernel(const Args a)
 
 // ----------------------------------------------------------------- host side
 
+// Whether out lies on some of q otherwise than as q itself: a workgroup would
+// write rows that another has yet to read.
+bool out_on_q(const Args &a)
+{
+    const Axis q[3] = {{a.batch, a.q_batch}, {a.tokens, a.q_token}, {a.heads, a.q_head}};
+    int64_t stride = a.c.dim;
+    bool same = a.q == a.out;
+    for (int i = 2; i >= 0; i--) {
+        same = same && (q[i].size == 1 || q[i].stride == stride);
+        stride *= q[i].size;
+    }
+    const uintptr_t from = (uintptr_t)a.out / 2;   // in values, whose addresses are even
+    return !same && rows_meet(from, (__int128)from + stride, (uintptr_t)a.q / 2, q, 3, a.c.dim);
+}
+
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 bool within(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
 constexpr int64_t kMost = 1ll << 30;
@@ -1974,6 +1990,7 @@ extern "C" int df11_quantized_attention(const df11_quantized_cache *c, const df1
     if (!a.rows) return DF11_OK;
     if (!aligned16(a.q) || !aligned16(a.out) || !a.lengths)
         return df11::fail(DF11_E_ARG, "%s: null or misaligned pointer", who);
+    if (out_on_q(a)) return df11::fail(DF11_E_ARG, "%s: out shares memory with q, and is not q itself", who);
     const uint64_t need = part_bytes(a);
     if (workspace_bytes < need || (need && !aligned16(workspace)))
         return df11::fail(DF11_E_ARG, "%s: the workspace must be 16-byte aligned and hold %llu bytes", who,

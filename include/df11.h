@@ -675,7 +675,7 @@ typedef struct df11_quantized_attention_args {
     const void *q;                /* [batch, tokens, heads, dim] */
     const int32_t *lengths;       /* [batch] */
     const int32_t *block_table;   /* [batch, table_pages], or NULL */
-    void *out;                    /* [batch, tokens, heads, dim], contiguous; may be q itself */
+    void *out;                    /* [batch, tokens, heads, dim], contiguous; may be q itself, no other of its memory */
     float *lse;                   /* [batch, tokens, heads], or NULL */
     int64_t batch, tokens, heads, table_pages, table_batch, q_batch, q_token, q_head;
     double scale;

@@ -13,3 +13,38 @@ def test_scales_that_would_leave_float32_are_refused(scale):
     L, c, a = _lib.lib(), _cache(), _attend(scale=scale)
     assert L.df11_quantized_attention(ctypes.byref(c), ctypes.byref(a), PTR, 1 << 40, None) == ARG
     assert b"scale" in L.df11_last_error()
+
+
+Q = 1 << 40   # an address that nothing follows
+
+
+def _refused(call, *args):
+    return call(*(ctypes.byref(a) for a in args)) == ARG and b"share" in _lib.lib().df11_last_error()
+
+
+def _attention(c, a):
+    # no workspace, which is looked at behind the memory that q and out share
+    return _lib.lib().df11_quantized_attention(c, a, None, 0, None)
+
+
+def _rows(q, batch, tokens, heads, dim, strides):
+    return {q + 2 * (b * strides[0] + t * strides[1] + h * strides[2] + d)
+            for b in range(batch) for t in range(tokens) for h in range(heads) for d in range(0, dim, 8)}
+
+
+@pytest.mark.parametrize("batch,tokens,heads,strides", [
+    (2, 3, 4, (768, 256, 64)), (2, 3, 4, (64, 0, 0)), (2, 3, 4, (0, 0, 64)), (3, 2, 2, (512, 256, 128)), (3, 2, 2, (128, 384, 64)),
+    (1, 1, 4, (8, 8, 64)), (2, 1, 2, (1024, 8, 64)), (4, 1, 2, (2048, 0, 512)), (1, 3, 2, (0, 64, 192)), (2, 2, 2, (0, 0, 0))])
+def test_out_on_q(batch, tokens, heads, strides):
+    """Every place of out against q's rows, one by one."""
+    own = batch * tokens * heads * 64
+    need = dict(batch=batch, tokens=tokens, heads=heads, q=Q, q_batch=strides[0], q_token=strides[1], q_head=strides[2], lengths=PTR,
+                block_table=PTR, table_pages=2000, table_batch=2000)
+    rows = _rows(Q, batch, tokens, heads, 64, strides)
+    sizes, dense = (batch, tokens, heads), (tokens * heads * 64, heads * 64, 64)
+    is_q = all(n == 1 or s == d for n, s, d in zip(sizes, strides, dense))
+    most = sum((n - 1) * s for n, s in zip(sizes, strides)) + 64
+    for at in list(range(-own - 16, most + 16, 8)):
+        out = Q + 2 * at
+        shares = any(x in rows for x in range(out, out + 2 * own, 16)) and not (at == 0 and is_q)
+        assert _refused(_attention, _cache(), _attend(out=out, **need)) == shares, at
