@@ -29,4 +29,31 @@ inline bool rows_meet(__int128 from, __int128 to, __int128 base, const Axis *axe
     return false;
 }
 
+// Whether two sets of blocks of `own` units, the second `apart` units behind
+// the first and both along the same two axes, meet.  The blocks of a set lie
+// apart: the axis of greater stride steps over all that the other one spans.
+inline bool sets_meet(__int128 apart, Axis great, Axis small, int64_t own)
+{
+    if (great.size <= 1) great = Axis{1, 0};
+    if (small.size <= 1) small = Axis{1, 0};
+    if (great.stride < small.stride) {
+        const Axis x = great;
+        great = small, small = x;
+    }
+    const auto whole = [](__int128 x, __int128 y) { return x / y - (x % y < 0); };   // rounded down
+    // along each axis only the two differences of places around the quotient can meet
+    for (int i = 0; i < (great.size > 1 ? 2 : 1); i++) {
+        const __int128 a = great.size > 1 ? whole(apart, great.stride) + i : 0;
+        if (a >= great.size || -a >= great.size) continue;
+        const __int128 rest = apart - a * great.stride;
+        for (int j = 0; j < (small.size > 1 ? 2 : 1); j++) {
+            const __int128 b = small.size > 1 ? whole(rest, small.stride) + j : 0;
+            if (b >= small.size || -b >= small.size) continue;
+            const __int128 left = rest - b * small.stride;
+            if (left < own && -left < own) return true;
+        }
+    }
+    return false;
+}
+
 }  // namespace df11serve

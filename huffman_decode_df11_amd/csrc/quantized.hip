@@ -1924,6 +1924,12 @@ extern "C" int df11_quantized_write(const df11_quantized_cache *cache, const df1
     if (!pages_apart(cache, cache->code_page, cache->code_head, slots * (a.c.dim / 2)) ||
         !pages_apart(cache, cache->scale_page, cache->scale_head, slots * a.c.groups * 2))
         return df11::fail(DF11_E_ARG, "%s: pages of the cache share memory", who);
+    const int64_t pages = cache->pages, heads = cache->kv_heads;
+    if (pages && (sets_meet((__int128)(uintptr_t)a.c.v_codes - (uintptr_t)a.c.k_codes, {pages, cache->code_page},
+                            {heads, cache->code_head}, slots * (a.c.dim / 2)) ||
+                  sets_meet(((__int128)(uintptr_t)a.c.v_scales - (uintptr_t)a.c.k_scales) / 2, {pages, cache->scale_page},
+                            {heads, cache->scale_head}, slots * a.c.groups * 2)))
+        return df11::fail(DF11_E_ARG, "%s: keys and values of the cache share memory", who);
     a.k = (const uint16_t *)p->k, a.v = (const uint16_t *)p->v;
     a.positions = p->positions, a.counts = p->counts, a.lengths = p->lengths;
     a.batch = p->batch, a.tokens = p->tokens;

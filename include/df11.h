@@ -625,7 +625,8 @@ typedef struct df11_quantized_cache {
  * stay as they are.  No two tokens of a call may go to the same row: what it
  * holds afterwards would be a mixture.  Errors: E_ARG (null or misaligned
  * pointer -- 16 bytes for k, v and the cache -- sizes or strides out of
- * range, pages that share memory, lengths on positions or counts), E_DEVICE. */
+ * range, pages, or keys and values, that share memory, lengths on positions or
+ * counts), E_DEVICE. */
 typedef struct df11_quantized_write_args {
     const void *k, *v;
     const int32_t *positions;     /* [batch] */

@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 from huffman_decode_df11_amd import _lib
-from test_host_quantized import ARG, PTR, _attend, _cache
+from test_host_quantized import ARG, PTR, _attend, _cache, _write
 
 
 @pytest.mark.parametrize("scale", [1e38, 3e38, -1e38])
@@ -48,3 +48,35 @@ def test_out_on_q(batch, tokens, heads, strides):
         out = Q + 2 * at
         shares = any(x in rows for x in range(out, out + 2 * own, 16)) and not (at == 0 and is_q)
         assert _refused(_attention, _cache(), _attend(out=out, **need)) == shares, at
+
+
+def _blocks(base, pages, heads, page_stride, head_stride, own):
+    return {x for p in range(pages) for h in range(heads)
+            for x in range(base + p * page_stride + h * head_stride, base + p * page_stride + h * head_stride + own, 16)}
+
+
+# heads in pages, pages in heads, with gaps that hold the other's blocks, and single ones
+@pytest.mark.parametrize("pages,heads,page_stride,head_stride", [
+    (3, 2, 1024, 512), (3, 2, 2048, 1024), (3, 2, 4096, 512), (2, 3, 512, 2048), (2, 3, 1024, 4096), (1, 4, 0, 1024), (4, 1, 1024, 0),
+    (1, 1, 0, 0), (3, 3, 3584, 1024)])
+@pytest.mark.parametrize("what", ["codes", "scales"])
+def test_keys_and_values_that_share_memory_are_not_written(pages, heads, page_stride, head_stride, what):
+    """Every place of the values against the keys' blocks, one by one: 16
+    positions of 32 bytes of codes, or of two pairs of scales (128 bytes)."""
+    by, own = (1, 512) if what == "codes" else (4, 128)
+    strides = dict(code_page=page_stride, code_head=head_stride, scale_page=page_stride // 8, scale_head=head_stride // 8)
+    keys = _blocks(Q, pages, heads, page_stride // by, head_stride // by, own)
+    reach = (pages * page_stride + heads * head_stride) // by + own
+    for apart in range(-reach, reach + 16, 16 * (1 if reach < 4000 else 3)):
+        places = dict(k_codes=Q, v_codes=Q + (1 << 30), k_scales=Q + (2 << 30), v_scales=Q + (3 << 30))
+        places["k_" + what], places["v_" + what] = Q, Q + apart
+        if what == "scales":
+            places["k_codes"] = Q + (2 << 30)
+        shares = bool(keys & _blocks(Q + apart, pages, heads, page_stride // by, head_stride // by, own))
+        c = _cache(pages=pages, kv_heads=heads, **strides, **places)
+        # what is right goes on to a launch that cannot be made: more tokens than one has threads for
+        w = _write(k=Q, v=Q, positions=Q, lengths=Q + 64, block_table=Q, tokens=1 << 29, k_batch=0, v_batch=0)
+        L = _lib.lib()
+        assert L.df11_quantized_write(ctypes.byref(c), ctypes.byref(w), None) == ARG
+        assert (b"keys and values" in L.df11_last_error()) == shares, apart
+        assert shares or b"one launch" in L.df11_last_error()
