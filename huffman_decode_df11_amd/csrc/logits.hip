@@ -14,6 +14,7 @@
 #include <algorithm>
 
 #include "df11_internal.h"
+#include "overlap.h"
 #include "serve_device.h"
 
 namespace {
@@ -235,6 +236,24 @@ __global__ void __launch_bounds__(kThreads, 6) adjust_kernel(const Args a)
     }
 }
 
+// Whether out lies on some of the logits otherwise than as the logits
+// themselves.  Rows of the same strides are compared place by place, of others by
+// where all of them lie.
+bool out_on_logits(const df11_adjust_logits_args *p)
+{
+    const bool one_batch = p->batch <= 1, one_row = p->tokens <= 1;
+    const Axis batch{p->batch, one_batch ? 0 : p->out_batch}, row{p->tokens, one_row ? 0 : p->out_token};
+    const Axis other_batch{p->batch, one_batch ? 0 : p->logits_batch}, other_row{p->tokens, one_row ? 0 : p->logits_token};
+    const int bytes = p->dtype == DF11_FP32 ? 4 : 2;
+    const __int128 out = (uintptr_t)p->out / bytes, logits = (uintptr_t)p->logits / bytes;
+    if (batch.stride == other_batch.stride && row.stride == other_row.stride)
+        return out != logits && sets_meet(out - logits, batch, row, p->vocab);
+    const auto end = [&](const Axis &x, const Axis &y) {
+        return (__int128)(x.size - 1) * x.stride + (__int128)(y.size - 1) * y.stride + p->vocab;
+    };
+    return out < logits + end(other_batch, other_row) && logits < out + end(batch, row);
+}
+
 int check(const df11_adjust_logits_args *p, Args &a)
 {
     const char *who = "df11_adjust_logits";
@@ -253,8 +272,6 @@ int check(const df11_adjust_logits_args *p, Args &a)
     const bool batches_apart = p->batch <= 1 || p->out_batch >= (p->tokens - 1) * p->out_token + p->vocab ||
                                (p->out_batch >= p->vocab && p->tokens > 1 && p->out_token >= (p->batch - 1) * p->out_batch + p->vocab);
     if (!rows_apart || !batches_apart) return df11::fail(DF11_E_ARG, "%s: rows of out share memory", who);
-    if (p->out == p->logits && p->batch && ((p->tokens > 1 && p->out_token != p->logits_token) || (p->batch > 1 && p->out_batch != p->logits_batch)))
-        return df11::fail(DF11_E_ARG, "%s: out lies on logits with other strides", who);
     a = Args{(const uint8_t *)p->logits, (uint8_t *)p->out, p->history, p->draft_tokens, p->bias_tokens, p->lengths,
              p->prompt_lengths, p->repetition, p->presence, p->frequency, p->bias_values, (const uint8_t *)p->mask,
              (int32_t)p->batch, (int32_t)p->tokens, (int32_t)p->vocab, (int32_t)p->history_tokens, (int32_t)p->biases, 1,
@@ -274,6 +291,7 @@ extern "C" int df11_adjust_logits(const df11_adjust_logits_args *p, void *stream
     const int rc = check(p, a);
     if (rc) return rc;
     if (!a.batch) return DF11_OK;
+    if (out_on_logits(p)) return df11::fail(DF11_E_ARG, "%s: out shares memory with the logits, and is not the logits", who);
     const uintptr_t mask = p->dtype == DF11_FP32 ? 3 : 1, wide = p->token_bytes - 1;
     if (!a.logits || !a.out || (((uintptr_t)a.logits | (uintptr_t)a.out) & mask) || ((uintptr_t)a.mask & 3) ||
         (a.history_tokens && (!a.history || !a.lengths)) || (a.biases && (!a.bias_tokens || !a.bias_values)) ||

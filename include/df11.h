@@ -700,7 +700,8 @@ int df11_quantized_attention(const df11_quantized_cache *c, const df11_quantized
  * of a token are taken in 64 bits, then rounded to float32 and to
  * the type; the sum of a token's biases is taken in their order.  NULL: no such
  * term (logits without any are copied).  mask: words of 32 bits, bit i % 32
- * of word i / 32.  out may be logits itself. */
+ * of word i / 32.  out may be logits itself (the same strides), or share no
+ * memory with it; with other strides neither may lie between the other's rows. */
 typedef struct df11_adjust_logits_args {
     const void *logits;           /* [batch, tokens, vocab], last axis contiguous */
     void *out;                    /* the same type; strides out_batch, out_token */
@@ -718,7 +719,7 @@ typedef struct df11_adjust_logits_args {
 
 /* batch and tokens at most 65535, vocab at most 2^22, biases at most 4096.
  * Errors: E_ARG (null or misaligned pointer, sizes or strides out of range,
- * out on logits with other strides), E_DEVICE. */
+ * rows of out that share memory, out on some of logits), E_DEVICE. */
 int df11_adjust_logits(const df11_adjust_logits_args *a, void *stream);
 
 /* ---------------------------------------------------------------- utilities */

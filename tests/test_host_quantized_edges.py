@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 from huffman_decode_df11_amd import _lib
-from test_host_quantized import ARG, PTR, _attend, _cache, _write
+from test_host_quantized import ARG, PTR, _attend, _cache, _logits, _write
 
 
 @pytest.mark.parametrize("scale", [1e38, 3e38, -1e38])
@@ -80,3 +80,35 @@ def test_keys_and_values_that_share_memory_are_not_written(pages, heads, page_st
         assert L.df11_quantized_write(ctypes.byref(c), ctypes.byref(w), None) == ARG
         assert (b"keys and values" in L.df11_last_error()) == shares, apart
         assert shares or b"one launch" in L.df11_last_error()
+
+
+@pytest.mark.parametrize("dtype,size", [(_lib.DF11_FP32, 4), (_lib.DF11_BF16, 2)])
+@pytest.mark.parametrize("batch,tokens,logits,out", [
+    (2, 3, (30, 10), (30, 10)), (2, 3, (60, 20), (60, 20)), (2, 3, (10, 40), (10, 40)), (2, 3, (70, 10), (70, 10)), (1, 4, (0, 25), (7, 25)),
+    (5, 1, (25, 3), (25, 0)), (1, 1, (5, 5), (9, 9)), (2, 3, (30, 10), (66, 20)), (2, 3, (0, 10), (30, 10)), (3, 2, (0, 0), (20, 10))])
+def test_out_on_logits(batch, tokens, logits, out, dtype, size):
+    """Rows of 10 tokens, every place of out against those of the logits, one by one."""
+    rows = lambda base, s: {base + size * (b * s[0] + t * s[1] + i) for b in range(batch) for t in range(tokens) for i in range(10)}  # noqa: E731
+    same = all(n == 1 or x == y for n, x, y in zip((batch, tokens), logits, out))
+    reach = 10 + sum((n - 1) * max(x, y) for n, x, y in zip((batch, tokens), logits, out)) + 3
+    for apart in range(-reach, reach + 1):
+        a, b = rows(Q, logits), rows(Q + size * apart, out)
+        # what is right goes on to a mask that is misaligned
+        x = _logits(logits=Q, out=Q + size * apart, dtype=dtype, batch=batch, tokens=tokens, vocab=10, logits_batch=logits[0],
+                    logits_token=logits[1], out_batch=out[0], out_token=out[1], mask=PTR + 2)
+        shares = bool(a & b) and apart != 0 if same else max(min(a), min(b)) <= min(max(a), max(b))   # of other strides: by where all lie
+        L = _lib.lib()
+        assert L.df11_adjust_logits(ctypes.byref(x), None) == ARG
+        assert (b"share" if shares else b"misaligned") in L.df11_last_error(), apart
+
+
+def test_out_between_the_rows_of_the_logits():
+    """Two halves of one allocation's rows: the same strides, nothing shared, refused for its launch only."""
+    L = _lib.lib()
+    x = _logits(logits=Q, out=Q + 4 * (1 << 22), batch=60000, tokens=1, vocab=1 << 22, logits_batch=1 << 23, out_batch=1 << 23, logits_token=0,
+                out_token=0, history_tokens=0)
+    assert L.df11_adjust_logits(ctypes.byref(x), None) == ARG and b"one launch" in L.df11_last_error()
+    for change in (dict(out=Q + 4 * ((1 << 22) - 1)), dict(out=Q + 4 * ((1 << 22) + 1)), dict(out=Q - 4)):
+        for n, v in change.items():
+            setattr(x, n, v)
+        assert L.df11_adjust_logits(ctypes.byref(x), None) == ARG and b"share" in L.df11_last_error()
