@@ -1963,6 +1963,8 @@ extern "C" int df11_quantized_read(const df11_quantized_cache *cache, const df11
     if (!p->batch || !p->count) return DF11_OK;
     if (!aligned16(p->k) || !aligned16(p->v) || !p->lengths)
         return df11::fail(DF11_E_ARG, "%s: null or misaligned pointer", who);
+    const __int128 own = (__int128)p->batch * p->count * a.c.kv_heads * a.c.dim * 2, apart = (__int128)(uintptr_t)p->v - (uintptr_t)p->k;
+    if (apart < own && -apart < own) return df11::fail(DF11_E_ARG, "%s: k and v share memory", who);
     a.k = (uint16_t *)p->k, a.v = (uint16_t *)p->v, a.first = p->first, a.lengths = p->lengths;
     a.batch = p->batch, a.count = p->count;
     int status = DF11_OK;

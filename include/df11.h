@@ -642,7 +642,8 @@ int df11_quantized_write(const df11_quantized_cache *c, const df11_quantized_wri
  * values they stand for, taken in float32 and rounded to the cache's type, those
  * of numbers past its greatest one to that (the step of a group is rounded, so
  * that code 15 may stand for more than what was written); zeros from
- * lengths[b] on and where nothing is held.  Errors as df11_quantized_write. */
+ * lengths[b] on and where nothing is held.  Errors as df11_quantized_write, and
+ * E_ARG for k and v that share memory. */
 typedef struct df11_quantized_read_args {
     void *k, *v;
     const int32_t *first;         /* [batch], or NULL */

@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 from huffman_decode_df11_amd import _lib
-from test_host_quantized import ARG, PTR, _attend, _cache, _logits, _write
+from test_host_quantized import ARG, PTR, _attend, _cache, _logits, _read, _write
 
 
 @pytest.mark.parametrize("scale", [1e38, 3e38, -1e38])
@@ -112,3 +112,18 @@ def test_out_between_the_rows_of_the_logits():
         for n, v in change.items():
             setattr(x, n, v)
         assert L.df11_adjust_logits(ctypes.byref(x), None) == ARG and b"share" in L.df11_last_error()
+
+
+def test_rows_read_back_to_one_place():
+    """k and v [2, 5, 2, 64]: what shares memory is refused, and what does not for its launch only."""
+    L, own = _lib.lib(), 2 * 5 * 2 * 64 * 2
+    for apart in (0, 16, own - 16, 16 - own):
+        r = _read(k=Q, v=Q + apart)
+        assert L.df11_quantized_read(ctypes.byref(_cache()), ctypes.byref(r), None) == ARG
+        assert b"k and v share memory" in L.df11_last_error()
+    count = 1 << 30
+    own = 2 * count * 2 * 64 * 2
+    for apart, what in ((own, b"one launch"), (-own, b"one launch"), (own - 16, b"share"), (16 - own, b"share")):
+        r = _read(k=Q * 4, v=Q * 4 + apart, count=count, lengths=Q)
+        assert L.df11_quantized_read(ctypes.byref(_cache()), ctypes.byref(r), None) == ARG
+        assert what in L.df11_last_error(), apart
