@@ -1917,8 +1917,11 @@ extern "C" int df11_quantized_write(const df11_quantized_cache *cache, const df1
     if (!strides_ok({p->k_batch, p->k_token, p->k_head, p->v_batch, p->v_token, p->v_head}))
         return df11::fail(DF11_E_ARG, "%s: strides must be multiples of 8", who);
     if (!p->batch) return DF11_OK;
-    if ((p->tokens && (!aligned16(p->k) || !aligned16(p->v))) || !p->positions || !p->lengths || p->lengths == p->positions ||
-        p->lengths == p->counts)
+    const auto on_lengths = [&](const int32_t *x) {
+        return x && (uintptr_t)x < (uintptr_t)(p->lengths + p->batch) && (uintptr_t)p->lengths < (uintptr_t)(x + p->batch);
+    };
+    if ((p->tokens && (!aligned16(p->k) || !aligned16(p->v))) || !p->positions || !p->lengths || on_lengths(p->positions) ||
+        on_lengths(p->counts))
         return df11::fail(DF11_E_ARG, "%s: null, misaligned or shared pointer", who);
     const int64_t slots = cache->page;
     if (!pages_apart(cache, cache->code_page, cache->code_head, slots * (a.c.dim / 2)) ||

@@ -127,3 +127,15 @@ def test_rows_read_back_to_one_place():
         r = _read(k=Q * 4, v=Q * 4 + apart, count=count, lengths=Q)
         assert L.df11_quantized_read(ctypes.byref(_cache()), ctypes.byref(r), None) == ARG
         assert what in L.df11_last_error(), apart
+
+
+@pytest.mark.parametrize("which", ["positions", "counts"])
+@pytest.mark.parametrize("apart,shares", [(0, True), (4, True), (-4, True), (8, False), (-8, False)])
+def test_lengths_on_what_they_are_made_of(which, apart, shares):
+    """Two sequences' lengths, which one workgroup each writes, against their positions or counts."""
+    L = _lib.lib()
+    w = _write(k=Q, v=Q, positions=Q, counts=Q + 64, lengths=Q + (0 if which == "positions" else 64) + apart, tokens=1 << 29, k_batch=0,
+               v_batch=0)
+    c = _cache(k_codes=Q, v_codes=Q + (1 << 30), k_scales=Q + (2 << 30), v_scales=Q + (3 << 30))
+    assert L.df11_quantized_write(ctypes.byref(c), ctypes.byref(w), None) == ARG
+    assert (b"shared pointer" in L.df11_last_error()) == shares and (shares or b"one launch" in L.df11_last_error())
