@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kMoveThreads) read_kernel(const ReadArgs a)
 // or 16 + c (fp16); what the 128 or 16 adds is taken off again through the
 // terms of the least values.
 //
-// A wave has 16 rows (NT tiles of them) and takes 32 keys at a time:
+// A wave has 16 rows and takes 32 keys at a time:
 //   S^T: v_mfma_f32_16x16x32, A = codes of key l % 16, dims of group i from
 //     the DP / 4 dims that lane l holds of it (place l / 16); the sums of
 //     group i times the keys' steps, which the lanes of a row of 16 share, are
@@ -465,12 +465,12 @@ struct Halves {
     uint32_t any;                // keys that some row sees
 };
 
-template <class E, int DP, int NT>
+template <class E, int DP>
 struct Wave {
     static constexpr int W = DP / 16, G = DP == 64 ? 2 : 4, KW = DP / 32, S = DP / 32;
-    f32x4 o[NT][W];
-    float least[NT][G];   // sums of p times what code 8 stands for, over this lane's keys
-    float m[NT], l[NT];
+    f32x4 o[W];
+    float least[G];   // sums of p times what code 8 stands for, over this lane's keys
+    float m, l;
     // In float16 V's steps go into the products times a power of two that leaves
     // the greatest so far (its bits at most `most`) below 1: as they are, 2^15
     // times a step of 2 would pass its range.  o holds sums of those.  bfloat16
@@ -479,8 +479,15 @@ struct Wave {
     float scale;
     uint32_t most;
 
+    __device__ __forceinline__ void begin()
+    {
+        m = -INFINITY, l = 0.0f, scale = 1.0f, most = 0;
+#pragma unroll
+        for (int j = 0; j < W; j++) o[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < G; i++) least[i] = 0.0f;
+    }
     // bits: steps of this lane, NaN and infinities left out
-    __device__ __forceinline__ void begin() { scale = 1.0f, most = 0; }
     __device__ __forceinline__ void raise_scale(uint32_t bits)
     {
 #pragma unroll
@@ -489,9 +496,7 @@ struct Wave {
         const float power = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, E::value(most)) & 0x7f800000u);
         const float next = 0.5f / power, by = next / scale;
 #pragma unroll
-        for (int t = 0; t < NT; t++)
-#pragma unroll
-            for (int j = 0; j < W; j++) o[t][j] *= by;
+        for (int j = 0; j < W; j++) o[j] *= by;
         scale = next;
     }
     static __device__ __forceinline__ uint32_t step_bits(uint32_t pair)
@@ -504,23 +509,15 @@ struct Wave {
 // One wave over the keys [key0, key1) of a head's pages, every step-th run of 32.
 // EVEN: each quarter of DP dims is there as a whole or not at all, so that a
 // lane's codes of K are one load.
-template <class E, int DP, int NT, bool EVEN>
-__device__ __forceinline__ void attend_wave(const Args &a, int b, int head, int n, const u32x4 (&q)[NT][DP / 32],
-                                            const u32x4 (&qb)[NT], const float (&qf)[NT], const int (&limit)[NT],
-                                            int key0, int key1, int step, Wave<E, DP, NT> &x)
+template <class E, int DP, bool EVEN>
+__device__ __forceinline__ void attend_wave(const Args &a, int b, int head, int n, const u32x4 (&q)[DP / 32], const u32x4 &qb,
+                                            float qf, int limit, int key0, int key1, int step, Wave<E, DP> &x)
 {
-    typedef Wave<E, DP, NT> X;
+    typedef Wave<E, DP> X;
     typedef Code<E> C;
     constexpr int W = X::W, G = X::G, KW = X::KW;
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-#pragma unroll
-    for (int k = 0; k < NT; k++) {
-        x.m[k] = -INFINITY, x.l[k] = 0.0f, x.begin();
-#pragma unroll
-        for (int j = 0; j < W; j++) x.o[k][j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < G; i++) x.least[k][i] = 0.0f;
-    }
+    x.begin();
     if (key0 >= key1) return;
     const int dim = a.c.dim, row_bytes = dim / 2, words = dim / 8;
     // Held in registers: as constants they would make two instructions of the mask-and-or.
@@ -607,26 +604,21 @@ __device__ __forceinline__ void attend_wave(const Args &a, int b, int head, int 
     load_v(now);
     for (int base = key0; base < key1; base += step) {
         const int next = base + step;
-        f32x4 s[NT][2], sum[NT][2][G];
+        f32x4 s[2], sum[2][G];
 #pragma unroll
         for (int k = 0; k < 2; k++) {
-#pragma unroll
-            for (int t = 0; t < NT; t++) {
-                const u32x4 pairs{kp[k][0], kp[k][1], G == 4 ? kp[k][G - 2] : 0, G == 4 ? kp[k][G - 1] : 0};
-                s[t][k] = E::mfma16(pairs, qb[t], f32x4{0, 0, 0, 0});
-            }
+            const u32x4 pairs{kp[k][0], kp[k][1], G == 4 ? kp[k][G - 2] : 0, G == 4 ? kp[k][G - 1] : 0};
+            s[k] = E::mfma16(pairs, qb, f32x4{0, 0, 0, 0});
 #pragma unroll
             for (int i = 0; i < G; i++) {
-#pragma unroll
-                for (int t = 0; t < NT; t++) sum[t][k][i] = f32x4{0, 0, 0, 0};
+                sum[k][i] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int f = 0; f < KW / G; f++) {
                     u32x4 codes;
 #pragma unroll
                     for (int w = 0; w < 4; w++)
                         codes[w] = G == 4 ? number(kx[k][4 * f + w], i) : number(kx[k][w / 2], i + 2 * (w & 1));
-#pragma unroll
-                    for (int t = 0; t < NT; t++) sum[t][k][i] = E::mfma16(codes, q[t][i * (KW / G) + f], sum[t][k][i]);
+                    sum[k][i] = E::mfma16(codes, q[i * (KW / G) + f], sum[k][i]);
                 }
             }
         }
@@ -640,12 +632,10 @@ __device__ __forceinline__ void attend_wave(const Args &a, int b, int head, int 
         load_k(then);
         __builtin_amdgcn_sched_barrier(0);   // add_scaled waits for the products above
 #pragma unroll
-        for (int t = 0; t < NT; t++)
-#pragma unroll
-            for (int k = 0; k < 2; k++) {
-                s[t][k] *= qf[t];
-                add_scaled<G>(s[t][k], kstep[k], sum[t][k]);
-            }
+        for (int k = 0; k < 2; k++) {
+            s[k] *= qf;
+            add_scaled<G>(s[k], kstep[k], sum[k]);
+        }
         const bool plain = base + 32 <= all && now.any == 0xffffffffu;   // uniform: every row sees every key
         float vstep[2], vleast[2];
         bool odd = false;
@@ -663,46 +653,41 @@ __device__ __forceinline__ void attend_wave(const Args &a, int b, int head, int 
         }
         if (!plain) {
 #pragma unroll
-            for (int t = 0; t < NT; t++)
-#pragma unroll
-                for (int k = 0; k < 2; k++)
-#pragma unroll
-                    for (int r = 0; r < 4; r++) {
-                        const int i = 16 * k + 4 * g + r;
-                        if (!(now.any >> i & 1) || base + i >= limit[t]) s[t][k][r] = -INFINITY;
-                    }
-        }
-        float p[NT][2][4];
-#pragma unroll
-        for (int t = 0; t < NT; t++) {
-            float mx = s[t][0][0];
-#pragma unroll
-            for (int k = 0; k < 2; k++)
-#pragma unroll
-                for (int r = 0; r < 4; r++) mx = fmaxf(mx, s[t][k][r]);
-            mx = over_rows(mx) * a.scale2;
-            // m is kLift below the running maximum, which is raised only past
-            // 2^8 times itself: the sums are seldom scaled
-            const float low = mx - E::kLift;
-            const bool raise = low > x.m[t] + 8.0f;
-            if (__any(raise)) {
-                const float f = raise ? exp2_fast(x.m[t] - low) : 1.0f;
-                x.m[t] = raise ? low : x.m[t];
-                x.l[t] *= f;
-#pragma unroll
-                for (int j = 0; j < W; j++) x.o[t][j] *= f;
-#pragma unroll
-                for (int i = 0; i < G; i++) x.least[t][i] *= f;
-            }
-            const float safe = x.m[t] == -INFINITY ? 0.0f : x.m[t];
-#pragma unroll
             for (int k = 0; k < 2; k++)
 #pragma unroll
                 for (int r = 0; r < 4; r++) {
-                    p[t][k][r] = exp2_fast(__builtin_fmaf(s[t][k][r], a.scale2, -safe));
-                    x.l[t] += p[t][k][r];
+                    const int i = 16 * k + 4 * g + r;
+                    if (!(now.any >> i & 1) || base + i >= limit) s[k][r] = -INFINITY;
                 }
         }
+        float mx = s[0][0];
+#pragma unroll
+        for (int k = 0; k < 2; k++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) mx = fmaxf(mx, s[k][r]);
+        mx = over_rows(mx) * a.scale2;
+        // m is kLift below the running maximum, which is raised only past
+        // 2^8 times itself: the sums are seldom scaled
+        const float low = mx - E::kLift;
+        const bool raise = low > x.m + 8.0f;
+        if (__any(raise)) {
+            const float f = raise ? exp2_fast(x.m - low) : 1.0f;
+            x.m = raise ? low : x.m;
+            x.l *= f;
+#pragma unroll
+            for (int j = 0; j < W; j++) x.o[j] *= f;
+#pragma unroll
+            for (int i = 0; i < G; i++) x.least[i] *= f;
+        }
+        const float safe = x.m == -INFINITY ? 0.0f : x.m;
+        float p[2][4];
+#pragma unroll
+        for (int k = 0; k < 2; k++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                p[k][r] = exp2_fast(__builtin_fmaf(s[k][r], a.scale2, -safe));
+                x.l += p[k][r];
+            }
         // Weight 0 times a step that is a number is 0.  Only where steps that
         // some rows must not see are no numbers, the query tokens take turns,
         // each with its unseen keys cleared and the sums of its own rows.
@@ -719,32 +704,29 @@ __device__ __forceinline__ void attend_wave(const Args &a, int b, int head, int 
                 for (int k = 0; k < 2; k++)
                     if (base + 16 * k + 4 * g + (G == 4 ? c >> 2 : (c & 7) >> 1) >= all + turn) step_now[k] = least_now[k] = 0.0f;
             }
-            u32x4 pb[NT][G];
+            u32x4 pb[G];
+            float before[G];
 #pragma unroll
-            for (int t = 0; t < NT; t++) {
-                float before[G];
+            for (int i = 0; i < G; i++) before[i] = x.least[i];
 #pragma unroll
-                for (int i = 0; i < G; i++) before[i] = x.least[t][i];
+            for (int k = 0; k < 2; k++) add_weighted<G>(x.least, least_now[k], p[k]);
+            const bool others = turns > 1 && limit != all + turn;   // this lane's row has another turn
+            if (turns > 1)
 #pragma unroll
-                for (int k = 0; k < 2; k++) add_weighted<G>(x.least[t], least_now[k], p[t][k]);
-                const bool others = turns > 1 && limit[t] != all + turn;   // this lane's row has another turn
+                for (int i = 0; i < G; i++) x.least[i] = others ? before[i] : x.least[i];
+            unroll<G>([&](auto i) {
+                float y[2][4];
+#pragma unroll
+                for (int k = 0; k < 2; k++)
+                    unroll<4>([&](auto r) {
+                        y[k][r] = p[k][r] * row_lane<decltype(r)::value * G + decltype(i)::value>(step_now[k]);
+                    });
+#pragma unroll
+                for (int w = 0; w < 4; w++) pb[i][w] = E::pack(y[w >> 1][2 * (w & 1)], y[w >> 1][2 * (w & 1) + 1]);
                 if (turns > 1)
 #pragma unroll
-                    for (int i = 0; i < G; i++) x.least[t][i] = others ? before[i] : x.least[t][i];
-                unroll<G>([&](auto i) {
-                    float y[2][4];
-#pragma unroll
-                    for (int k = 0; k < 2; k++)
-                        unroll<4>([&](auto r) {
-                            y[k][r] = p[t][k][r] * row_lane<decltype(r)::value * G + decltype(i)::value>(step_now[k]);
-                        });
-#pragma unroll
-                    for (int w = 0; w < 4; w++) pb[t][i][w] = E::pack(y[w >> 1][2 * (w & 1)], y[w >> 1][2 * (w & 1) + 1]);
-                    if (turns > 1)
-#pragma unroll
-                        for (int w = 0; w < 4; w++) pb[t][i][w] = others ? 0 : pb[t][i][w];
-                });
-            }
+                    for (int w = 0; w < 4; w++) pb[i][w] = others ? 0 : pb[i][w];
+            });
             // byte v of two keys' words, in the low bytes of the halves; the
             // second product of each takes the codes' offset and 8 off
             const u32x4 mid{C::kMidBits, C::kMidBits, C::kMidBits, C::kMidBits};
@@ -757,11 +739,8 @@ __device__ __forceinline__ void attend_wave(const Args &a, int b, int head, int 
                     const uint32_t y = __builtin_amdgcn_perm(vx[2 * w + 1][v / 4], vx[2 * w][v / 4], sel);
                     low[w] = number(y, 0), high[w] = number(y, 1);
                 }
-#pragma unroll
-                for (int t = 0; t < NT; t++) {
-                    x.o[t][2 * v] = E::mfma16(mid, pb[t][2 * v % G], E::mfma16(low, pb[t][2 * v % G], x.o[t][2 * v]));
-                    x.o[t][2 * v + 1] = E::mfma16(mid, pb[t][(2 * v + 1) % G], E::mfma16(high, pb[t][(2 * v + 1) % G], x.o[t][2 * v + 1]));
-                }
+                x.o[2 * v] = E::mfma16(mid, pb[2 * v % G], E::mfma16(low, pb[2 * v % G], x.o[2 * v]));
+                x.o[2 * v + 1] = E::mfma16(mid, pb[(2 * v + 1) % G], E::mfma16(high, pb[(2 * v + 1) % G], x.o[2 * v + 1]));
             }
         }
         load_v(then);
@@ -832,18 +811,14 @@ __device__ __forceinline__ float over_blocks(float x, F &&join)
 // the order of the products, its sums' parts first.
 template <class E, int DP, bool FULL, class F>
 __device__ __forceinline__ void attend_few(const Args &a, int b, int head, int n, const uint32_t *q, F &&prepare, int limit,
-                                           int key0, int key1, int step, Wave<E, DP, 1> &x)
+                                           int key0, int key1, int step, Wave<E, DP> &x)
 {
-    typedef Wave<E, DP, 1> X;
+    typedef Wave<E, DP> X;
     typedef Code<E> C;
     constexpr int W = X::W, G = X::G, kWords = DP / 8;
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-    float &m = x.m[0], &l = x.l[0];
-    m = -INFINITY, l = 0.0f, x.begin();
-#pragma unroll
-    for (int j = 0; j < W; j++) x.o[0][j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < G; i++) x.least[0][i] = 0.0f;
+    float &m = x.m, &l = x.l;
+    x.begin();
     const int dim = FULL ? DP : a.c.dim, row_bytes = dim / 2, words = dim / 8;
     uint32_t mask_bits = C::kMask, off_bits = C::kOffBits;
     asm("" : "+s"(mask_bits));
@@ -983,9 +958,9 @@ __device__ __forceinline__ void attend_few(const Args &a, int b, int head, int n
             m = raise ? low : m;
             l *= f;
 #pragma unroll
-            for (int j = 0; j < W; j++) x.o[0][j] *= f;
+            for (int j = 0; j < W; j++) x.o[j] *= f;
 #pragma unroll
-            for (int i = 0; i < G; i++) x.least[0][i] *= f;
+            for (int i = 0; i < G; i++) x.least[i] *= f;
         }
         const float safe = m == -INFINITY ? 0.0f : m;
         float p[4];
@@ -1007,16 +982,16 @@ __device__ __forceinline__ void attend_few(const Args &a, int b, int head, int n
                 constexpr int k = decltype(i)::value;
                 const float wide = hidden ? 0.0f : E::value(vp[k] & 0xffffu);
                 const float least = hidden ? 0.0f : __builtin_fmaf(8.0f, wide, E::value(vp[k] >> 16));
-                const float before = x.least[0][k], narrow = X::kScaled ? wide * x.scale : wide;
+                const float before = x.least[k], narrow = X::kScaled ? wide * x.scale : wide;
                 float z[4];
                 unroll<4>([&](auto r) {
                     constexpr int at = decltype(r)::value;
                     z[at] = p[at] * quad_lane<at>(narrow);
-                    x.least[0][k] = __builtin_fmaf(quad_lane<at>(least), p[at], x.least[0][k]);
+                    x.least[k] = __builtin_fmaf(quad_lane<at>(least), p[at], x.least[k]);
                 });
                 y[k][0] = E::pack(z[0], z[1]), y[k][1] = E::pack(z[2], z[3]);
                 if (turns > 1)
-                    y[k][0] = others ? 0 : y[k][0], y[k][1] = others ? 0 : y[k][1], x.least[0][k] = others ? before : x.least[0][k];
+                    y[k][0] = others ? 0 : y[k][0], y[k][1] = others ? 0 : y[k][1], x.least[k] = others ? before : x.least[k];
             });
             const u32x4 mid{C::kMidBits, C::kMidBits, C::kMidBits, C::kMidBits};
 #pragma unroll
@@ -1040,8 +1015,8 @@ __device__ __forceinline__ void attend_few(const Args &a, int b, int head, int n
                             const uint32_t both = __builtin_amdgcn_perm(vx[8 * u + 2 * w + 1][v / 4], vx[8 * u + 2 * w][v / 4], sel);
                             lower[w] = number(both, 0), upper[w] = number(both, 1);
                         }
-                        x.o[0][2 * v] = E::mfma16(mid, pb[0], E::mfma16(lower, pb[0], x.o[0][2 * v]));
-                        x.o[0][2 * v + 1] = E::mfma16(mid, pb[1], E::mfma16(upper, pb[1], x.o[0][2 * v + 1]));
+                        x.o[2 * v] = E::mfma16(mid, pb[0], E::mfma16(lower, pb[0], x.o[2 * v]));
+                        x.o[2 * v + 1] = E::mfma16(mid, pb[1], E::mfma16(upper, pb[1], x.o[2 * v + 1]));
                     }
                 }
         }
@@ -1066,46 +1041,42 @@ __device__ __forceinline__ void put_lse(const Args &a, int64_t row, float m, flo
 }
 
 // The sums of a row's workgroup: each wave's in LDS, joined and written out.
-template <class E, int DP, int NT>
-__device__ __forceinline__ void join_waves(const Args &a, Wave<E, DP, NT> &x, int b, int head, int split, int row0, int row_count)
+template <class E, int DP>
+__device__ __forceinline__ void join_waves(const Args &a, Wave<E, DP> &x, int b, int head, int split, int row0, int row_count)
 {
-    typedef Wave<E, DP, NT> X;
+    typedef Wave<E, DP> X;
     constexpr int W = X::W, G = X::G;
     __shared__ float join_o[kWaves][16][DP + 4];
     __shared__ float2 join_ml[kWaves][16];
     const float unscale = X::kScaled ? 1.0f / x.scale : 1.0f;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
+    if (g == 0) join_ml[wave][c] = make_float2(x.m, x.l);
 #pragma unroll
-    for (int t = 0; t < NT; t++) {
-        if (t) __syncthreads();
-        if (g == 0) join_ml[wave][c] = make_float2(x.m[t], x.l[t]);
+    for (int r = 0; r < 4; r++)
 #pragma unroll
-        for (int r = 0; r < 4; r++)
+        for (int j = 0; j < W; j++) join_o[wave][c][(4 * g + r) * W + j] = __builtin_fmaf(x.o[j][r], unscale, x.least[j % G]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * (DP / 2); i += 64 * kWaves) {
+        const int r = i / (DP / 2), d = 2 * (i % (DP / 2)), at = row0 + r;
+        if (at >= row_count || d >= a.c.dim) continue;
+        float mm = -INFINITY, ll = 0.0f, u = 0.0f, v = 0.0f;
 #pragma unroll
-            for (int j = 0; j < W; j++) join_o[wave][c][(4 * g + r) * W + j] = __builtin_fmaf(x.o[t][j][r], unscale, x.least[t][j % G]);
-        __syncthreads();
-        for (int i = threadIdx.x; i < 16 * (DP / 2); i += 64 * kWaves) {
-            const int r = i / (DP / 2), d = 2 * (i % (DP / 2)), at = row0 + 16 * t + r;
-            if (at >= row_count || d >= a.c.dim) continue;
-            float mm = -INFINITY, ll = 0.0f, u = 0.0f, v = 0.0f;
+        for (int w = 0; w < kWaves; w++) mm = fmaxf(mm, join_ml[w][r].x);
+        const float safe = mm == -INFINITY ? 0.0f : mm;
 #pragma unroll
-            for (int w = 0; w < kWaves; w++) mm = fmaxf(mm, join_ml[w][r].x);
-            const float safe = mm == -INFINITY ? 0.0f : mm;
-#pragma unroll
-            for (int w = 0; w < kWaves; w++) {
-                const float f = exp2_fast(join_ml[w][r].x - safe);
-                ll += f * join_ml[w][r].y;
-                u += f * join_o[w][r][d], v += f * join_o[w][r][d + 1];
-            }
-            const int64_t row = ((int64_t)b * a.tokens + at / a.group) * a.heads + head * a.group + at % a.group;
-            const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-            if (a.splits == 1) {
-                *(uint32_t *)(a.out + row * a.c.dim + d) = E::pack(u * inv, v * inv);
-                if (d == 0) put_lse(a, row, mm, ll);
-            } else {
-                *(float2 *)(a.part_o + (split * a.rows + row) * a.c.dim + d) = make_float2(u * inv, v * inv);
-                if (d == 0) a.part_ml[split * a.rows + row] = make_float2(mm, ll);
-            }
+        for (int w = 0; w < kWaves; w++) {
+            const float f = exp2_fast(join_ml[w][r].x - safe);
+            ll += f * join_ml[w][r].y;
+            u += f * join_o[w][r][d], v += f * join_o[w][r][d + 1];
+        }
+        const int64_t row = ((int64_t)b * a.tokens + at / a.group) * a.heads + head * a.group + at % a.group;
+        const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+        if (a.splits == 1) {
+            *(uint32_t *)(a.out + row * a.c.dim + d) = E::pack(u * inv, v * inv);
+            if (d == 0) put_lse(a, row, mm, ll);
+        } else {
+            *(float2 *)(a.part_o + (split * a.rows + row) * a.c.dim + d) = make_float2(u * inv, v * inv);
+            if (d == 0) a.part_ml[split * a.rows + row] = make_float2(mm, ll);
         }
     }
 }
@@ -1151,72 +1122,64 @@ __device__ __forceinline__ Item item_of(const Args &a)
     return x;
 }
 
-template <class E, int DP, int NT, bool EVEN>
+template <class E, int DP, bool EVEN>
 __global__ void __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 2) attend_kernel(const Args a)
 {
-    typedef Wave<E, DP, NT> X;
-    constexpr int G = X::G, KW = X::KW, kRows = 16 * NT;
+    typedef Wave<E, DP> X;
+    constexpr int G = X::G, KW = X::KW, kRows = 16;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
     const Item it = item_of(a);
     if (!it.some) return;
     const int row_count = a.tokens * a.group;
-    u32x4 q[NT][DP / 32], qb[NT];
-    float qf[NT];
-    int limit[NT];
+    const int row = it.tile * kRows + c;
+    const int token = row / a.group, h = it.head * a.group + row % a.group;
+    const uint16_t *from = a.q + it.b * a.q_batch + min(token, a.tokens - 1) * a.q_token + h * a.q_head;
+    u32x4 q[DP / 32], qb;
+    float sum[G];
 #pragma unroll
-    for (int t = 0; t < NT; t++) {
-        const int row = it.tile * kRows + 16 * t + c;
-        const int token = row / a.group, h = it.head * a.group + row % a.group;
-        limit[t] = it.n - a.tokens + 1 + token;
-        const uint16_t *from = a.q + it.b * a.q_batch + min(token, a.tokens - 1) * a.q_token + h * a.q_head;
-        float sum[G];
+    for (int i = 0; i < G; i++) sum[i] = 0.0f;
+    // word w of this lane's dims: eight dims, i and i + 4 in group i mod G
 #pragma unroll
-        for (int i = 0; i < G; i++) sum[i] = 0.0f;
-        // word w of this lane's dims: eight dims, i and i + 4 in group i mod G
+    for (int w = 0; w < KW; w++) {
+        const int d = 8 * (KW * g + w);
+        const u32x4 y = *(const u32x4 *)(from + min(d, a.c.dim - 8));   // no branch around the loads
+        const bool some = row < row_count && d < a.c.dim;
 #pragma unroll
-        for (int w = 0; w < KW; w++) {
-            const int d = 8 * (KW * g + w);
-            const u32x4 y = *(const u32x4 *)(from + min(d, a.c.dim - 8));   // no branch around the loads
-            const bool some = row < row_count && d < a.c.dim;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                uint32_t both = __builtin_amdgcn_perm(y[2 + i / 2], y[i / 2], i & 1 ? 0x07060302u : 0x05040100u);
-                both = some ? both : 0;
-                sum[i % G] += E::value(both & 0xffffu) + E::value(both >> 16);
-                if (G == 4) q[t][i * (KW / G) + w / 4][w % 4] = both;
-                else q[t][i % 2][2 * w + i / 2] = both;
-            }
+        for (int i = 0; i < 4; i++) {
+            uint32_t both = __builtin_amdgcn_perm(y[2 + i / 2], y[i / 2], i & 1 ? 0x07060302u : 0x05040100u);
+            both = some ? both : 0;
+            sum[i % G] += E::value(both & 0xffffu) + E::value(both >> 16);
+            if (G == 4) q[i * (KW / G) + w / 4][w % 4] = both;
+            else q[i % 2][2 * w + i / 2] = both;
         }
-        float most = 0.0f, inverse;
-#pragma unroll
-        for (int i = 0; i < G; i++) {
-            sum[i] += __shfl_xor(sum[i], 16);
-            sum[i] += __shfl_xor(sum[i], 32);
-            most = fmaxf(most, fabsf(sum[i]));
-        }
-        qf[t] = power_below<E>(most, inverse);
-#pragma unroll
-        for (int i = 0; i < 4; i++) qb[t][i] = i < G && g < 3 ? part_pair<E>(sum[i % G] * inverse, g) : 0;
     }
+    float most = 0.0f, inverse;
+#pragma unroll
+    for (int i = 0; i < G; i++) {
+        sum[i] += __shfl_xor(sum[i], 16);
+        sum[i] += __shfl_xor(sum[i], 32);
+        most = fmaxf(most, fabsf(sum[i]));
+    }
+    const float qf = power_below<E>(most, inverse);
+#pragma unroll
+    for (int i = 0; i < 4; i++) qb[i] = i < G && g < 3 ? part_pair<E>(sum[i % G] * inverse, g) : 0;
     X x;
-    attend_wave<E, DP, NT, EVEN>(a, it.b, it.head, it.n, q, qb, qf, limit, it.key0 + kStep * wave, it.key1, kStep * kWaves, x);
+    attend_wave<E, DP, EVEN>(a, it.b, it.head, it.n, q, qb, qf, it.n - a.tokens + 1 + token, it.key0 + kStep * wave, it.key1,
+                             kStep * kWaves, x);
+    x.l += __shfl_xor(x.l, 16);
+    x.l += __shfl_xor(x.l, 32);
 #pragma unroll
-    for (int t = 0; t < NT; t++) {
-        x.l[t] += __shfl_xor(x.l[t], 16);
-        x.l[t] += __shfl_xor(x.l[t], 32);
-#pragma unroll
-        for (int i = 0; i < G; i++) {
-            x.least[t][i] += __shfl_xor(x.least[t][i], 16);
-            x.least[t][i] += __shfl_xor(x.least[t][i], 32);
-        }
+    for (int i = 0; i < G; i++) {
+        x.least[i] += __shfl_xor(x.least[i], 16);
+        x.least[i] += __shfl_xor(x.least[i], 32);
     }
-    join_waves<E, DP, NT>(a, x, it.b, it.head, it.split, it.tile * kRows, row_count);
+    join_waves<E, DP>(a, x, it.b, it.head, it.split, it.tile * kRows, row_count);
 }
 
 template <class E, int DP, bool FULL>
 __global__ void __launch_bounds__(64 * kWaves, DP == 256 ? 2 : DP == 128 ? 3 : 4) few_kernel(const Args a)
 {
-    typedef Wave<E, DP, 1> X;
+    typedef Wave<E, DP> X;
     constexpr int G = X::G;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Item it = item_of(a);
@@ -1272,10 +1235,10 @@ __global__ void __launch_bounds__(64 * kWaves, DP == 256 ? 2 : DP == 128 ? 3 : 4
     attend_few<E, DP, FULL>(a, it.b, it.head, it.n, q[row], prepare, it.n - a.tokens + 1 + token, it.key0 + kFewStep * wave,
                             it.key1, kFewStep * kWaves, x);
     const auto add = [](float u, float v) { return u + v; };
-    x.l[0] = over_blocks(x.l[0], add);
+    x.l = over_blocks(x.l, add);
 #pragma unroll
-    for (int i = 0; i < G; i++) x.least[0][i] = over_blocks(x.least[0][i], add);
-    join_waves<E, DP, 1>(a, x, it.b, it.head, it.split, 0, row_count);
+    for (int i = 0; i < G; i++) x.least[i] = over_blocks(x.least[i], add);
+    join_waves<E, DP>(a, x, it.b, it.head, it.split, 0, row_count);
 }
 
 // Many rows: a workgroup of NW waves has 32 rows a wave, and all share the
@@ -2023,8 +1986,8 @@ extern "C" int df11_quantized_attention(const df11_quantized_cache *c, const df1
         else if (a.many) hipLaunchKernelGGL((tile_kernel<E, DP, tile_waves(DP), false>), dim3((uint32_t)items), dim3(64 * tile_waves(DP)), 0, st, a);
         else if (a.few && a.c.dim == DP) hipLaunchKernelGGL((few_kernel<E, DP, true>), dim3((uint32_t)items), block, 0, st, a);
         else if (a.few) hipLaunchKernelGGL((few_kernel<E, DP, false>), dim3((uint32_t)items), block, 0, st, a);
-        else if (even) hipLaunchKernelGGL((attend_kernel<E, DP, 1, true>), dim3((uint32_t)items), block, 0, st, a);
-        else hipLaunchKernelGGL((attend_kernel<E, DP, 1, false>), dim3((uint32_t)items), block, 0, st, a);
+        else if (even) hipLaunchKernelGGL((attend_kernel<E, DP, true>), dim3((uint32_t)items), block, 0, st, a);
+        else hipLaunchKernelGGL((attend_kernel<E, DP, false>), dim3((uint32_t)items), block, 0, st, a);
         if (!joins) return;
         if (a.wide) hipLaunchKernelGGL((join_kernel<E, true>), dim3((uint32_t)joins), block, 0, st, a);
         else hipLaunchKernelGGL((join_kernel<E, false>), dim3((uint32_t)joins), block, 0, st, a);
