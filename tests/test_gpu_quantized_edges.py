@@ -177,3 +177,34 @@ def test_finite_rows_are_read_back_finite(dtype):
         assert torch.equal(torch.isnan(got), torch.isnan(w)) and torch.equal(got.nan_to_num(), w.nan_to_num())
     assert torch.isfinite(k[:2]).all() and float(k[:2].max()) == top
     assert not torch.isfinite(k[6, ::2]).any() and not k[6, 1::2].any() and not torch.isfinite(k[7, 1::2]).any()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("T", [1, 20, 65, 200])
+def test_lse_of_large_logits(T, dtype):
+    """Logits of hundreds (bfloat16: thousands) against their own bound, which
+    keys held in one number of the type would leave."""
+    g = _gen(T)
+    parts = _held(_randn(g, 14, 1, 16, 128, dtype=dtype), _randn(g, 14, 1, 16, 128, dtype=dtype))
+    q = _randn(g, 1, T, 2, 128, dtype=dtype, scale=100.0 if dtype == HF else 1000.0)
+    n, scale = 201, 128 ** -0.5
+    table = torch.randperm(14, generator=g).view(1, 14).to(I32)
+    _, lse, want = _check(q, parts, [n], table, (T, dtype))
+    at = table[0].long()
+    k = ref.values(parts[0][at, 0], parts[2][at, 0]).flatten(0, 1)[:n]
+    step = ref.spread(parts[2][at, 0][..., 0].double(), 128).flatten(0, 1)[:n]
+    size = q[0].double().abs()
+    # A logit is a float32 sum of terms up to a step times the offset and 15, taken off again, and of values: 16 roundings
+    # of the whole each.  Many rows: K's values in two numbers of the type, made in float32 from 16 + a code.
+    u = ref.UNIT[dtype]
+    logit = 2.0 ** -20 * (step * (ref.OFF[dtype] + 15.0) + k.abs())
+    if 2 * T > MANY:
+        logit = logit + u * u * k.abs() + 2.0 ** -19 * step
+    # the greatest of the row's logits' errors; the exponentials' and sums'; m and the logarithm beside it in float32
+    bound = scale * (size @ logit.t()).amax(-1) + 2.0 ** -16 + 2.0 ** -22 * want[0].abs()
+    assert bool(((lse - want)[0].abs() <= bound).all()), float(((lse - want)[0].abs() / bound).max())
+    once = k.to(dtype).double()
+    seen = torch.arange(n) < n - T + 1 + torch.arange(T).view(T, 1, 1)
+    rough = torch.logsumexp((scale * q[0].double() @ once.t()).masked_fill(~seen, -INF), -1)
+    if 2 * T > MANY:
+        assert float(((rough - want[0]).abs() > bound).double().mean()) > 0.5
