@@ -279,7 +279,7 @@ class Generator:
         def adjust(logits):
             wishes = dict(self.wishes)
             if "mask" in wishes:
-                wishes["mask"] = wishes["mask"].expand(*logits.shape[:-1], -1).contiguous()
+                wishes["mask"] = wishes["mask"].expand(*logits.shape[:-1], -1)   # read with strides of 0
             return serve.adjust_logits(logits, self.history, lengths, prompt_lengths=self.prompt_lengths, drafts=drafts,
                                        out=logits, **wishes)
 
