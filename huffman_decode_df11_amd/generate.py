@@ -331,7 +331,10 @@ class Generator:
         return self.model.probs(self.model(ids, self.start + own, attend), self.temperature, adjust)
 
     def round(self):
-        """Tokens that every sequence gains [B, drafts + 1], -1 behind them, and how many drafts were taken [B]."""
+        """Tokens that every sequence gains [B, drafts + 1], -1 behind them, and how many drafts were taken [B].
+        Raises ValueError, before anything is done, where a sequence has no room for all of them."""
+        if int(self.own_count.max()) + self.drafts + 1 > self.room:
+            raise ValueError("the sequences' own positions are full: more room is needed")
         drafts, q = self.draft()
         p = self.score(torch.cat([self.last[:, None], drafts], 1))
         uniforms = torch.rand((self.batch, self.drafts + 1), generator=self.random, device=p.device)
@@ -351,8 +354,6 @@ class Generator:
         of drafts taken in a round."""
         out, taken, rounds = [[] for _ in range(self.batch)], 0.0, 0
         while min(len(s) for s in out) < count:
-            if int(self.own_count.max()) + self.drafts + 1 > self.room:
-                raise ValueError("the sequences' own positions are full: more room is needed")
             tokens, n = self.round()
             for s, row in zip(out, tokens.tolist()):
                 s.extend(t for t in row if t >= 0)

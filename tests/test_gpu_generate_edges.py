@@ -39,3 +39,20 @@ def test_masks_are_not_copied(model, monkeypatch, drafts):
     out, _ = g.generate(6)
     assert seen and set(seen) == {g.wishes["mask"].data_ptr()}
     assert all(t % 3 != 1 for s in out for t in s)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_rounds_end_with_the_room(model, bits):
+    """A round that might pass the page table or the history is refused, and leaves everything as it was."""
+    g = _generator(model, drafts=2, room=11, cache_bits=bits, wishes=generate.Wishes(presence=0.1))
+    rounds = 0
+    with pytest.raises(ValueError, match="more room"):
+        while rounds < 12:
+            g.round()
+            rounds += 1
+            assert int(g.own_count.max()) <= 11
+    assert rounds >= 3
+    before = [t.clone() for t in (g.own_count, g.history, g.last)]
+    with pytest.raises(ValueError, match="more room"):
+        g.round()
+    assert all(torch.equal(a, b) for a, b in zip(before, (g.own_count, g.history, g.last)))
