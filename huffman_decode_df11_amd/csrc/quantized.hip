@@ -1405,8 +1405,10 @@ __global__ void __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) tile_kernel(const 
         lds_barrier();
         const bool apart = __builtin_bit_cast(float, top) > 0x1p20f * __builtin_bit_cast(float, bottom);
         const int power = (int)(top >> 23) - 127 + 5;   // a range without values: -122
-        // Far apart: as they are, for the small ones' sake, but for what float16 would not hold
-        if (!apart || std::is_same_v<E, Fp16>) v_scale = __builtin_ldexpf(1.0f, min(14 - power, apart ? 0 : 126));
+        // Far apart: as they are, for the small ones' sake, but for what float16 would
+        // not hold, or float32's sum of 2^30 of them, each held up to 2^8 high
+        constexpr int kApart = std::is_same_v<E, Fp16> ? 14 : 88;
+        v_scale = __builtin_ldexpf(1.0f, apart ? min(kApart - power, 0) : min(14 - power, 126));
         return !apart;
     };
     // The values of a word's eight codes.

@@ -665,9 +665,9 @@ int df11_quantized_read(const df11_quantized_cache *c, const df11_quantized_read
  * for their greatest, where no group of a range reaches 2^20 times as far as
  * another, else to the type (K's values, and V's of a float16 cache, are held to
  * twice as many bits).
- * Up to 112 rows, or where V is so far apart, values of V past 2^115 / n over n
- * positions may come out infinite or NaN (sums of n probabilities, held up to
- * 2^8 high, times a step and 128 + a code), and float16 holds a probability times a step to 2^-31 of
+ * Up to 112 rows values of V past 2^115 / n over n positions may come out infinite
+ * or NaN (sums of n probabilities, held up to 2^8 high, times a step and 128 + a
+ * code), and float16 holds a probability times a step to 2^-31 of
  * the greatest step among a sequence's positions, seen or not.
  * K may be what any finite row is written as; scale is positive and below
  * 2^125; logits past float32's range are no numbers.

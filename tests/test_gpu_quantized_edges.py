@@ -208,3 +208,23 @@ def test_lse_of_large_logits(T, dtype):
     rough = torch.logsumexp((scale * q[0].double() @ once.t()).masked_fill(~seen, -INF), -1)
     if 2 * T > MANY:
         assert float(((rough - want[0]).abs() > bound).double().mean()) > 0.5
+
+
+@pytest.mark.parametrize("n", [70, 3000])
+@pytest.mark.parametrize("seen", ["by all", "by some", "by the last"])
+def test_many_rows_over_bfloat16_values_from_end_to_end(seen, n):
+    """One position's V reaches bfloat16's greatest number, and its greatest
+    code stands for more; the others' are of a size near 1 and come out as such where it is not seen."""
+    g = _gen(n)
+    per, T = -(-n // 16), 65
+    at = dict(zip(("by all", "by some", "by the last"), (n - T - 3, n - 30, n - 1)))[seen]
+    v = _randn(g, per, 1, 16, 64)
+    top = float(torch.finfo(BF).max)
+    table = torch.randperm(per, generator=g).view(1, per).to(I32)
+    page = int(table[0, at // 16])
+    v[page, 0, at % 16, :2], v[page, 0, at % 16, 2:4] = top, -2.0 ** 120
+    parts = _held(_randn(g, per, 1, 16, 64), v)
+    assert float((15 * parts[3][..., 0].double() + parts[3][..., 1].double()).max()) > top
+    got, _, _ = _check(_randn(g, 1, T, 2, 64), parts, [n], table, (seen, n))
+    before = got[0, :max(0, at - (n - T))]
+    assert not before.numel() or float(before.abs().max()) < 8.0
