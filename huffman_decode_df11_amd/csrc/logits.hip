@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 6) adjust_kernel(const Args a)
     typedef typename T::type type;
     constexpr int V = 16 / sizeof(type), kVecs = kPart / V / kThreads;
     struct Vec { type x[V]; };
-    extern __shared__ uint32_t words[];   // [kPart], the list, then the part's biases in their order
+    extern __shared__ __align__(16) uint32_t words[];   // [kPart], the list, then the part's biases in their order
     __shared__ int listed, wave_biases[kThreads / 64];
     uint16_t *const list = (uint16_t *)(words + kPart);
     Bias *const biases = (Bias *)(list + kPart);
