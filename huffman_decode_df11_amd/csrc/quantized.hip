@@ -285,16 +285,16 @@ __global__ void __launch_bounds__(kMoveThreads) read_kernel(const ReadArgs a)
             if (there[r]) {
                 const uint32_t low = w[which][r] & 0x0f0f0f0fu, high = w[which][r] >> 4 & 0x0f0f0f0fu;
                 float step[G], least[G], x[8];
-                bool past = false;   // a code may stand for more than the type's greatest number, since the step is rounded
+                float most = 0.0f;   // a code may stand for more than the type's greatest number, since the step is rounded
 #pragma unroll
                 for (int i = 0; i < G; i++) {
                     step[i] = E::value(pairs[which][r][i] & 0xffffu), least[i] = E::value(pairs[which][r][i] >> 16);
-                    past = past || __builtin_fabsf(__builtin_fmaf(15.0f, step[i], least[i])) > E::kMost;
+                    most = __builtin_fmaxf(most, __builtin_fabsf(__builtin_fmaf(15.0f, step[i], least[i])));
                 }
 #pragma unroll
                 for (int i = 0; i < 8; i++)
                     x[i] = __builtin_fmaf((float)((i % 2 ? high : low) >> (8 * (i / 2)) & 255u), step[i % G], least[i % G]);
-                if (past)
+                if (most > E::kMost)
 #pragma unroll
                     for (int i = 0; i < 8; i++)
                         if (__builtin_fabsf(step[i % G]) <= E::kMost && __builtin_fabsf(least[i % G]) <= E::kMost)
