@@ -251,7 +251,7 @@ def quantized_write(cache: QuantizedCache, k, v, positions, *, counts=None, bloc
     page block_table[b, s // page] (int32; page b alone when None); what lies
     outside the table or the cache is not written.  A group of values with a
     NaN or an infinity among them becomes NaN.  No two tokens of a call may go
-    to the same row.  Returns the lengths behind the new tokens, positions +
+    to the same row, and the cache's keys and values share no memory.  Returns the lengths behind the new tokens, positions +
     counts [B] int32."""
     if _elsewhere(cache.k_codes, stream):
         with _there(cache.k_codes, stream):
@@ -262,8 +262,9 @@ def quantized_write(cache: QuantizedCache, k, v, positions, *, counts=None, bloc
 def quantized_read(cache: QuantizedCache, lengths, count: int, *, first=None, block_table=None, out=None, stream=None):
     """`count` positions of every sequence back as 16-bit rows, from first[b]
     on (int32; 0 when None): k, v [B, count, Hkv, D], zeros from lengths[b]
-    (int32) on and where the table holds no page.  out: a pair of such
-    tensors to write to."""
+    (int32) on and where the table holds no page.  A code that stands for more
+    than the type's greatest number is read as that.  out: a pair of such
+    tensors to write to, which share no memory."""
     if _elsewhere(cache.k_codes, stream):
         with _there(cache.k_codes, stream):
             return quantized_read(cache, lengths, count, first=first, block_table=block_table, out=out)
@@ -275,7 +276,8 @@ def quantized_attention(q, cache: QuantizedCache, lengths, *, block_table=None, 
     """Attention over a quantised cache, whose values are taken as their codes
     stand for them.  q [B, T, Hq, D]: the last T of each sequence's lengths[b]
     positions (int32); token t sees the first lengths - T + 1 + t of them.
-    Returns out [B, T, Hq, D], and with return_lse also lse [B, T, Hq]
+    Returns out [B, T, Hq, D] (which may be q itself, but shares no other memory
+    with it), and with return_lse also lse [B, T, Hq]
     float32.  A row that sees no position is zero (lse -inf).  Values of V stay
     below 2^115 / lengths in size: past that up to 112 rows may come out infinite or NaN."""
     if _elsewhere(cache.k_codes, stream):
@@ -300,7 +302,7 @@ def adjust_logits(logits, history=None, lengths=None, *, prompt_lengths=None, dr
     int32 ([B, ceil(V / 32)] for logits [B, V]): a token whose bit is 0 gets
     -inf; a row may have none left.  Tokens int32 or int64, all alike;
     lengths int32; repetition, presence and frequency [B] float32.  Returns
-    out, which may be logits itself."""
+    out, which may be logits itself, but shares no other memory with it."""
     if _elsewhere(logits, stream):
         with _there(logits, stream):
             return adjust_logits(logits, history, lengths, prompt_lengths=prompt_lengths, drafts=drafts, repetition=repetition,

@@ -228,3 +228,27 @@ def test_many_rows_over_bfloat16_values_from_end_to_end(seen, n):
     got, _, _ = _check(_randn(g, 1, T, 2, 64), parts, [n], table, (seen, n))
     before = got[0, :max(0, at - (n - T))]
     assert not before.numel() or float(before.abs().max()) < 8.0
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("dtype,D", [(BF, 64), (HF, 128), (BF, 256)])
+def test_no_numbers_behind_a_tiles_last_key(dtype, D, bad):
+    """The first position that a tile's last row does not see has no number for
+    V (or no value but 0): the rows before it are the same to the bit, of several tiles and ranges."""
+    g = _gen(D)
+    T, page = 160, 16
+    tokens = 32 if D == 256 else 64
+    for n in (197, 1500):
+        per = -(-n // page)
+        parts = _held(_randn(g, per, 1, page, D, dtype=dtype), _randn(g, per, 1, page, D, dtype=dtype))
+        table = torch.randperm(per, generator=g).view(1, per).to(I32)
+        q, lengths = _randn(g, 1, T, 4, D, dtype=dtype).cuda(), torch.tensor([n], dtype=I32).cuda()
+        for first in (tokens, 2 * tokens, T - 1):
+            s = n - T + first
+            outs = []
+            for x in (0.0, bad):
+                changed = [p.clone() for p in parts]
+                changed[3][table[0, s // page].long(), :, s % page] = x
+                outs.append(serve.quantized_attention(q, _on_gpu(changed), lengths, block_table=table.cuda()))
+            assert torch.equal(outs[0][:, :first], outs[1][:, :first]) and torch.isfinite(outs[0]).all(), (n, first)
+            assert not torch.isfinite(outs[1][:, first:]).any(), (n, first)
