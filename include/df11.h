@@ -598,7 +598,7 @@ int df11_verify_drafts(const df11_verify_args *a, void *workspace, uint64_t work
  * above, dim d in group d mod G.  With a group's least and greatest value:
  *
  *   step   = (greatest - least) / 15, rounded to float32, then to `dtype`
- *   code_d = floor((x_d - least) / step + 1/2), from 0 to 15 (0 where step is 0)
+ *   code_d = floor((x_d - least) / step + 1/2) in 64 bits, from 0 to 15 (0 where step is 0)
  *
  * and the code stands for code_d * step + least.  A group that holds a NaN
  * or an infinity gets a step and a least value of NaN; what comes of a group
@@ -664,7 +664,8 @@ int df11_quantized_read(const df11_quantized_cache *c, const df11_quantized_read
  * the probabilities and the values of V: to float16, those times a power of two
  * for their greatest, where no group of a range reaches 2^20 times as far as
  * another, else to the type (K's values, and V's of a float16 cache, are held to
- * twice as many bits).
+ * twice as many bits); there a value of V is also off by up to 2^-13 of its step
+ * where it is made.
  * Up to 112 rows values of V past 2^115 / n over n positions may come out infinite
  * or NaN (sums of n probabilities, held up to 2^8 high, times a step and 128 + a
  * code), and float16 holds a probability times a step to 2^-31 of
