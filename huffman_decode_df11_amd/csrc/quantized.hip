@@ -108,12 +108,14 @@ __device__ __forceinline__ i16x2 over_lanes(i16x2 x, F &&join)
 // A code is floor((x - least) / step + 1/2): the quotient by the inverse, with
 // 2^-18 more than 1/2 (x - least and the inverse err by 2^-23 of at most 16),
 // has the code or one more as its floor, and (code - 1/2) * step, 13 bits, says
-// which.  64 bits are taken where x - least is not exact, which is seldom, or the step so small
-// that its inverse may not be a number.  The difference d is exact if d +
-// least is x again and least is no larger than x, or is larger but not
-// below 2^-8 of the step: x is at most 2^12 times it then, and all are multiples
-// of 2^-11 of it or more, which 24 bits hold.  (A smaller one, but 0, vanishes in d and
-// in d + least alike, and a value on a border has the code below: all of such a row in 64 bits.)
+// which.  64 bits are taken where the difference d = x - least is not exact, which
+// is seldom, or the step so small that its inverse may not be a number.  Of a least
+// value as great in size as x or greater d is exact if d + least is x again.  Of a smaller
+// one it is if that is 0, or not below 2^-8 of the step: both are multiples of
+// 2^(e - 10), 2^e its power of two, and d is at most 22.5 steps (a subnormal step's
+// rounding; else 15.1), so below 2^(e + 14): 24 bits.  (One that is
+// smaller still vanishes in d and in d + least alike, and a value on a border
+// would have the code above the formula's: all of such a row is taken in 64 bits.)
 template <class E, int DP>
 __device__ __forceinline__ void quantise(const u32x4 (&raw)[2], u32x2 &codes, uint32_t (&pairs)[RowLanes<DP>::G])
 {
